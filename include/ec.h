@@ -92,6 +92,7 @@ typedef enum ec_error {
 #define EC_S_BAD_CODEBOOK 0x10u     /* device codebook build: a code would exceed EC_MAX_CODE_LEN
                                        bits (or a count is 2^55 or more); the table is unusable
                                        (codec 0) and encodes that use it set this bit too */
+#define EC_S_BAD_OFFSETS 0x20u      /* grouped product: row offsets decrease or leave [0, m] */
 
 typedef enum ec_codec {
     EC_CODEC_QLC = 1,
@@ -510,6 +511,146 @@ int bf16_exp_encode(const uint8_t table[7], const uint16_t *d_in, uint64_t n, ui
  */
 int bf16_exp_decode(const uint8_t *d_in, uint64_t in_len, uint16_t *d_out, uint64_t n, uint32_t *d_status,
                     hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators of the feed-forward layers whose tensors the codecs carry: matrix
+ * products with a fused epilogue, dense or grouped by expert, and layer norm,
+ * each with its backward pass.  Tensors are row-major with a row stride in
+ * elements; a row's elements are contiguous.  Row strides, and pointers down
+ * to the element's own alignment, are free; 16-byte aligned pointers with row
+ * strides and row lengths that are multiples of 16 bytes are read in place,
+ * any other factor of a product is first copied into the workspace (rows
+ * padded to 16 bytes).  Sizes up to 2^31 - 1.
+ * ------------------------------------------------------------------------- */
+
+typedef enum ec_dtype {
+    EC_BF16 = 1,           /* bfloat16 */
+    EC_E4M3 = 2,           /* OCP FP8 E4M3FN: no infinities, NaN 0x7F/0xFF, largest 448 */
+    EC_FP32 = 3
+} ec_dtype;
+
+typedef enum ec_act {
+    EC_ACT_NONE = 0,
+    EC_ACT_GELU = 1,       /* z Phi(z), the exact (erf) form */
+    EC_ACT_SILU = 2,       /* z / (1 + e^-z) */
+    EC_ACT_RELU = 3        /* max(z, 0); slope 0 at 0 */
+} ec_act;
+
+#define EC_MAX_GROUPS 4096 /* experts of a grouped product */
+
+/*
+ * Arguments of the products.  x [m, k], w [n, k] (a row per output column),
+ * y [m, n].  Zero-initialise, then fill in what a function names; pointers it
+ * does not name may be NULL.
+ *
+ * Grouped (groups > 0): group e's rows are offsets[e] .. offsets[e + 1) - 1
+ * of the m rows (device int32[groups + 1], never decreasing, within [0, m];
+ * read on the device, never by the host), and it has its own w, bias and
+ * w_scale: w [groups, n, k], bias [groups, n], w_scale [groups, w_scales].
+ * Empty groups are fine.  Rows of no group get zeros in y, preact and dx.
+ * Offsets that decrease or leave [0, m] set EC_S_BAD_OFFSETS in *d_status;
+ * they then count as the running maximum, clamped to [0, m].
+ */
+typedef struct ec_linear_args {
+    uint64_t m, n, k;
+    uint32_t groups;               /* 0: one product */
+    uint32_t dtype;                /* of x and w: EC_BF16, or EC_E4M3 (forward only) */
+    uint32_t out_dtype;            /* of y (EC_BF16, EC_E4M3, EC_FP32) or of dw (EC_BF16, EC_FP32) */
+    uint32_t act;                  /* ec_act */
+    uint32_t bias_dtype;           /* EC_BF16 or EC_FP32 */
+    uint32_t x_scales;             /* x_scale entries: 1, or m (one per row) */
+    uint32_t w_scales;             /* w_scale entries per group: 1, or n (one per output column) */
+    uint32_t reserved;
+    const int32_t *d_offsets;
+    const void *d_x;
+    uint64_t x_stride;
+    const void *d_w;
+    uint64_t w_stride, w_group_stride;
+    const void *d_bias;            /* or NULL */
+    const void *d_residual;        /* bf16 [m, n], or NULL */
+    uint64_t residual_stride;
+    const float *d_x_scale;        /* or NULL: 1 */
+    const float *d_w_scale;        /* or NULL: 1 */
+    const float *d_out_scale;      /* one factor before the cast to EC_E4M3, or NULL: 1 */
+    void *d_y;
+    uint64_t y_stride;
+    void *d_preact;                /* bf16: [m, n] written by linear_forward, or [m, k] read by linear_grad_input; or NULL */
+    uint64_t preact_stride;
+    const void *d_dy;              /* bf16 [m, n] */
+    uint64_t dy_stride;
+    void *d_dx;                    /* bf16 [m, k] */
+    uint64_t dx_stride;
+    void *d_dw;                    /* [n, k] or [groups, n, k], or NULL */
+    uint64_t dw_stride, dw_group_stride;
+    float *d_db;                   /* fp32 [n] or [groups, n] (contiguous), or NULL */
+    uint32_t *d_status;            /* or NULL */
+    void *d_workspace;             /* linear_workspace_bytes(), 16-byte aligned; may be NULL where that is 0 */
+    uint64_t workspace_bytes;
+} ec_linear_args;
+
+typedef enum ec_linear_op {
+    EC_LINEAR_FORWARD = 0,
+    EC_LINEAR_GRAD_INPUT = 1,
+    EC_LINEAR_GRAD_WEIGHT = 2
+} ec_linear_op;
+
+/* Bytes of workspace the call needs with these arguments (sizes, types,
+ * strides and pointers filled in; workspace ignored).  0 on bad arguments
+ * too: the call itself reports them. */
+uint64_t linear_workspace_bytes(const ec_linear_args *a, uint32_t op);
+
+/*
+ * z[m, n] = x_scale[m] w_scale[n] sum_k x[m, k] w[n, k] + bias[n]
+ * preact  = bf16(z)                                    (when d_preact)
+ * y       = out_dtype(act(z) + residual[m, n])         (EC_E4M3: times *d_out_scale, saturating, ties to even)
+ * Products and sums in fp32; one rounding, at the store.  Asynchronous on
+ * `stream`; allocates nothing.
+ */
+int linear_forward(const ec_linear_args *a, hipStream_t stream);
+
+/*
+ * dx[m, k] = act'(preact[m, k]) sum_n dy[m, n] w[n, k]
+ * for bf16 dy, w; preact (bf16) is the input of the activation that made x,
+ * required unless act is EC_ACT_NONE.  Reads d_dy, d_w, d_preact; writes d_dx.
+ */
+int linear_grad_input(const ec_linear_args *a, hipStream_t stream);
+
+/*
+ * dw[n, k] = sum_m dy[m, n] x[m, k]   (out_dtype EC_BF16 or EC_FP32)
+ * db[n]    = sum_m dy[m, n]           (fp32)
+ * over each group's rows, fixed order of summation.  Reads d_dy, d_x; writes
+ * d_dw and d_db, whichever is given.
+ */
+int linear_grad_weight(const ec_linear_args *a, hipStream_t stream);
+
+/*
+ * Layer norm over the rows of x [rows, cols] (EC_BF16 or EC_FP32):
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   y = (x - mean) rstd weight + bias     in out_dtype (EC_E4M3: times *d_out_scale, saturating)
+ * weight and bias are [cols] of type w_dtype (EC_BF16 or EC_FP32), each or
+ * both NULL for 1 and 0.  d_mean and d_rstd (fp32 [rows]) may be NULL.
+ * Statistics in fp32 from the centred values.  cols up to 65536.
+ */
+int layer_norm_forward(const void *d_x, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_stride,
+                       const void *d_weight, const void *d_bias, uint32_t w_dtype, float eps, void *d_y,
+                       uint32_t out_dtype, uint64_t y_stride, const float *d_out_scale, float *d_mean,
+                       float *d_rstd, hipStream_t stream);
+
+/* Workspace of layer_norm_grad. */
+uint64_t layer_norm_grad_workspace_bytes(uint64_t rows, uint64_t cols);
+
+/*
+ * Backward of layer_norm_forward.  With h = (x - mean) rstd and t = dy weight:
+ *   dx = rstd (t - mean_c(t) - h mean_c(t h)) + dres
+ *   dweight = sum_rows dy h,  dbias = sum_rows dy      (fp32, fixed order)
+ * dy, x, dres, dx are of type dtype (EC_BF16 or EC_FP32); dres may be NULL,
+ * and so may d_dx, or d_dweight and d_dbias (each).
+ */
+int layer_norm_grad(const void *d_dy, uint64_t dy_stride, const void *d_x, uint64_t x_stride, uint32_t dtype,
+                    uint64_t rows, uint64_t cols, const float *d_mean, const float *d_rstd,
+                    const void *d_weight, uint32_t w_dtype, const void *d_dres, uint64_t dres_stride, void *d_dx,
+                    uint64_t dx_stride, float *d_dweight, float *d_dbias, void *d_workspace,
+                    uint64_t workspace_bytes, hipStream_t stream);
 
 /* Static text for an ec_error value or for a set of EC_S_* status bits. */
 const char *ec_error_string(int code);

@@ -23,12 +23,15 @@ __all__ = [
     "encode_batch_device", "decode_batch_device", "huffman_tables_from_streams", "qlc_optimal_area_layout",
     "bf16_exp_table_from_counts", "bf16_exp_table_from_sigma", "bf16_exp_max_encoded_bytes", "bf16_exp_encode",
     "bf16_exp_decode", "byte_histogram_sized", "encode_sized", "encode_batch_sized",
+    "linear", "linear_backward", "grouped_linear", "grouped_linear_backward", "layer_norm", "layer_norm_backward",
+    "S_BAD_OFFSETS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libec.so")
 
 CODEC_QLC, CODEC_HUFFMAN, CODEC_EXP_GOLOMB = 1, 2, 3
 S_CAPACITY, S_CORRUPT, S_BAD_HEADER, S_CODEBOOK_MISMATCH, S_BAD_CODEBOOK = 0x1, 0x2, 0x4, 0x8, 0x10
+S_BAD_OFFSETS = 0x20
 MAX_BATCH = 128
 
 # QLC area layouts (symbols per area, suffix bits per area)
@@ -82,6 +85,15 @@ EXPORTS = {
     "bf16_exp_max_encoded_bytes": (_u64, [_u64, _u32]),
     "bf16_exp_encode": (_int, [_u8p, _vp, _u64, _u32, _vp, _u64, _vp, _vp, _vp]),
     "bf16_exp_decode": (_int, [_vp, _u64, _vp, _u64, _vp, _vp]),
+    "linear_workspace_bytes": (_u64, [_vp, _u32]),
+    "linear_forward": (_int, [_vp, _vp]),
+    "linear_grad_input": (_int, [_vp, _vp]),
+    "linear_grad_weight": (_int, [_vp, _vp]),
+    "layer_norm_forward": (_int, [_vp, _u32, _u64, _u64, _u64, _vp, _vp, _u32, ctypes.c_float, _vp, _u32, _u64, _vp,
+                                  _vp, _vp, _vp]),
+    "layer_norm_grad_workspace_bytes": (_u64, [_u64, _u64]),
+    "layer_norm_grad": (_int, [_vp, _u64, _vp, _u64, _u32, _u64, _u64, _vp, _vp, _vp, _u32, _vp, _u64, _vp, _u64,
+                               _vp, _vp, _vp, _u64, _vp]),
     "ec_error_string": (ctypes.c_char_p, [_int]),
     "ec_status_string": (ctypes.c_char_p, [_u32]),
 }
@@ -581,3 +593,7 @@ def pmf_kl(p_counts: torch.Tensor, q_counts: torch.Tensor, q_add: int = 0, out: 
         out = torch.empty(p.shape[0], dtype=torch.float32, device=p_counts.device)
     _check(lib().pmf_kl(_ptr(p), p.shape[0], _ptr(q_counts), int(q_add), _ptr(out), _stream(stream)), "pmf_kl")
     return out
+
+
+from .ffn import (grouped_linear, grouped_linear_backward, layer_norm, layer_norm_backward, linear,  # noqa: E402
+                  linear_backward)

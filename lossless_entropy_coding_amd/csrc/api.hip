@@ -298,6 +298,7 @@ const char *ec_status_string(uint32_t st) {
     if (st & EC_S_CODEBOOK_MISMATCH) return "stream made with another codebook";
     if (st & EC_S_CORRUPT) return "corrupt stream";
     if (st & EC_S_CAPACITY) return "output capacity exceeded";
+    if (st & EC_S_BAD_OFFSETS) return "row offsets of a grouped product decrease or leave the rows";
     return "unknown status";
 }
 

@@ -1,0 +1,269 @@
+// C ABI of the feed-forward operators: argument checks and launches.
+#include <string.h>
+
+#include "ffn_common.h"
+
+namespace ec {
+namespace {
+
+constexpr uint64_t kMaxSize = (1ull << 31) - 1;
+
+uint64_t size_of(uint32_t dtype) { return dtype == EC_FP32 ? 4 : dtype == EC_BF16 ? 2 : dtype == EC_E4M3 ? 1 : 0; }
+
+// A [rows, cols] tensor that may be absent: aligned to its element, with room
+// for a row in its stride.
+bool tensor_ok(const void *p, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t stride) {
+    const uint64_t s = size_of(dtype);
+    return s && ((uintptr_t)p & (s - 1)) == 0 && (rows <= 1 || stride >= cols) && stride < (1ull << 40);
+}
+
+// As tensor_ok, and present unless it has no elements.
+bool factor_ok(const void *p, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t stride) {
+    return (p || !rows || !cols) && tensor_ok(p, dtype, rows, cols, stride);
+}
+
+bool common_ok(const ec_linear_args *a) {
+    if (!a || a->m > kMaxSize || a->n > kMaxSize || a->k > kMaxSize || a->act > EC_ACT_RELU) return false;
+    if (a->groups > EC_MAX_GROUPS || (a->groups && (!a->d_offsets || ((uintptr_t)a->d_offsets & 3)))) return false;
+    return ((uintptr_t)a->d_status & 3) == 0 && ((uintptr_t)a->d_workspace & 15) == 0;
+}
+
+bool group_stride_ok(const ec_linear_args *a, uint64_t rows, uint64_t cols, uint64_t stride, uint64_t group) {
+    if (a->groups <= 1 || !rows || !cols) return true;
+    return group >= (rows - 1) * stride + cols && group < (1ull << 48);
+}
+
+int check_forward(const ec_linear_args *a) {
+    if (!common_ok(a)) return EC_E_INVAL;
+    if (a->dtype != EC_BF16 && a->dtype != EC_E4M3) return EC_E_INVAL;
+    if (!size_of(a->out_dtype)) return EC_E_INVAL;
+    if (!factor_ok(a->d_x, a->dtype, a->m, a->k, a->x_stride)) return EC_E_INVAL;
+    if (!factor_ok(a->d_w, a->dtype, a->n, a->k, a->w_stride)) return EC_E_INVAL;
+    if (!group_stride_ok(a, a->n, a->k, a->w_stride, a->w_group_stride)) return EC_E_INVAL;
+    if (!factor_ok(a->d_y, a->out_dtype, a->m, a->n, a->y_stride)) return EC_E_INVAL;
+    if (a->d_bias && ((a->bias_dtype != EC_BF16 && a->bias_dtype != EC_FP32) ||
+                      !tensor_ok(a->d_bias, a->bias_dtype, 1, a->n, a->n)))
+        return EC_E_INVAL;
+    if (!tensor_ok(a->d_residual, EC_BF16, a->m, a->n, a->d_residual ? a->residual_stride : a->n)) return EC_E_INVAL;
+    if (!tensor_ok(a->d_preact, EC_BF16, a->m, a->n, a->d_preact ? a->preact_stride : a->n)) return EC_E_INVAL;
+    if (a->d_x_scale && a->x_scales != 1 && a->x_scales != a->m) return EC_E_INVAL;
+    if (a->d_w_scale && a->w_scales != 1 && a->w_scales != a->n) return EC_E_INVAL;
+    if (((uintptr_t)a->d_x_scale | (uintptr_t)a->d_w_scale | (uintptr_t)a->d_out_scale) & 3) return EC_E_INVAL;
+    if (a->d_out_scale && a->out_dtype != EC_E4M3) return EC_E_INVAL;
+    return EC_OK;
+}
+
+int check_grad_input(const ec_linear_args *a) {
+    if (!common_ok(a) || a->dtype != EC_BF16) return EC_E_INVAL;
+    if (!factor_ok(a->d_dy, EC_BF16, a->m, a->n, a->dy_stride)) return EC_E_INVAL;
+    if (!factor_ok(a->d_w, EC_BF16, a->n, a->k, a->w_stride)) return EC_E_INVAL;
+    if (!group_stride_ok(a, a->n, a->k, a->w_stride, a->w_group_stride)) return EC_E_INVAL;
+    if (!factor_ok(a->d_dx, EC_BF16, a->m, a->k, a->dx_stride)) return EC_E_INVAL;
+    if (a->act != EC_ACT_NONE && !factor_ok(a->d_preact, EC_BF16, a->m, a->k, a->preact_stride)) return EC_E_INVAL;
+    return EC_OK;
+}
+
+int check_grad_weight(const ec_linear_args *a) {
+    if (!common_ok(a) || a->dtype != EC_BF16) return EC_E_INVAL;
+    if (!factor_ok(a->d_dy, EC_BF16, a->m, a->n, a->dy_stride)) return EC_E_INVAL;
+    if (a->d_dw) {
+        if (a->out_dtype != EC_BF16 && a->out_dtype != EC_FP32) return EC_E_INVAL;
+        if (!factor_ok(a->d_x, EC_BF16, a->m, a->k, a->x_stride)) return EC_E_INVAL;
+        if (!factor_ok(a->d_dw, a->out_dtype, a->n, a->k, a->dw_stride)) return EC_E_INVAL;
+        if (!group_stride_ok(a, a->n, a->k, a->dw_stride, a->dw_group_stride)) return EC_E_INVAL;
+    }
+    return ((uintptr_t)a->d_db & 3) == 0 ? EC_OK : EC_E_INVAL;
+}
+
+int hip_code(hipError_t e) { return e == hipSuccess ? EC_OK : EC_E_HIP; }
+
+ProductArgs product(const ec_linear_args *a, uint32_t op) {
+    ProductArgs p;
+    memset(&p, 0, sizeof(p));
+    p.op = op;
+    p.dtype = a->dtype;
+    p.groups = a->groups;
+    p.offsets = a->d_offsets;
+    p.status = a->d_status;
+    p.preact = (uint16_t *)a->d_preact;
+    p.preact_stride = a->preact_stride;
+    if (op == EC_LINEAR_FORWARD) {
+        p.I = (uint32_t)a->m;
+        p.J = (uint32_t)a->n;
+        p.C = (uint32_t)a->k;
+        p.a = a->d_x;
+        p.a_i = a->x_stride;
+        p.a_c = 1;
+        p.b = a->d_w;
+        p.b_j = a->w_stride;
+        p.b_c = 1;
+        p.b_group = a->w_group_stride;
+        p.act = a->act;
+        p.out_dtype = a->out_dtype;
+        p.bias_dtype = a->bias_dtype;
+        p.x_scales = a->x_scales;
+        p.w_scales = a->w_scales;
+        p.bias = a->d_bias;
+        p.residual = (const uint16_t *)a->d_residual;
+        p.residual_stride = a->residual_stride;
+        p.x_scale = a->d_x_scale;
+        p.w_scale = a->d_w_scale;
+        p.out_scale = a->d_out_scale;
+        p.out = a->d_y;
+        p.out_stride = a->y_stride;
+    } else if (op == EC_LINEAR_GRAD_INPUT) {
+        p.I = (uint32_t)a->m;
+        p.J = (uint32_t)a->k;
+        p.C = (uint32_t)a->n;
+        p.a = a->d_dy;
+        p.a_i = a->dy_stride;
+        p.a_c = 1;
+        p.b = a->d_w;
+        p.b_j = 1;
+        p.b_c = a->w_stride;
+        p.b_group = a->w_group_stride;
+        p.act = a->act;
+        p.out_dtype = EC_BF16;
+        p.out = a->d_dx;
+        p.out_stride = a->dx_stride;
+    } else {
+        p.I = (uint32_t)a->n;
+        p.J = (uint32_t)a->k;
+        p.C = (uint32_t)a->m;
+        p.a = a->d_dy;
+        p.a_i = 1;
+        p.a_c = a->dy_stride;
+        p.b = a->d_x;
+        p.b_j = 1;
+        p.b_c = a->x_stride;
+        p.out_dtype = a->out_dtype;
+        p.out = a->d_dw;
+        p.out_stride = a->dw_stride;
+        p.out_group = a->dw_group_stride;
+    }
+    return p;
+}
+
+}  // namespace
+}  // namespace ec
+
+using namespace ec;
+
+uint64_t linear_workspace_bytes(const ec_linear_args *a, uint32_t op) {
+    (void)a;
+    (void)op;
+    return 0;
+}
+
+int linear_forward(const ec_linear_args *a, hipStream_t stream) {
+    const int rc = check_forward(a);
+    if (rc) return rc;
+    return hip_code(launch_product(product(a, EC_LINEAR_FORWARD), stream));
+}
+
+int linear_grad_input(const ec_linear_args *a, hipStream_t stream) {
+    const int rc = check_grad_input(a);
+    if (rc) return rc;
+    return hip_code(launch_product(product(a, EC_LINEAR_GRAD_INPUT), stream));
+}
+
+int linear_grad_weight(const ec_linear_args *a, hipStream_t stream) {
+    const int rc = check_grad_weight(a);
+    if (rc) return rc;
+    if (a->d_dw) {
+        const hipError_t e = launch_product(product(a, EC_LINEAR_GRAD_WEIGHT), stream);
+        if (e != hipSuccess) return EC_E_HIP;
+    }
+    if (!a->d_db) return EC_OK;
+    ColumnSumArgs c;
+    memset(&c, 0, sizeof(c));
+    c.dy = (const uint16_t *)a->d_dy;
+    c.dy_stride = a->dy_stride;
+    c.m = (uint32_t)a->m;
+    c.n = (uint32_t)a->n;
+    c.groups = a->groups;
+    c.offsets = a->d_offsets;
+    c.db = a->d_db;
+    c.parts = 1;
+    c.status = a->d_status;
+    return hip_code(launch_column_sum(c, stream));
+}
+
+int layer_norm_forward(const void *d_x, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_stride,
+                       const void *d_weight, const void *d_bias, uint32_t w_dtype, float eps, void *d_y,
+                       uint32_t out_dtype, uint64_t y_stride, const float *d_out_scale, float *d_mean,
+                       float *d_rstd, hipStream_t stream) {
+    if ((dtype != EC_BF16 && dtype != EC_FP32) || !cols || cols > 65536 || rows > kMaxSize || !size_of(out_dtype))
+        return EC_E_INVAL;
+    if ((d_weight || d_bias) && w_dtype != EC_BF16 && w_dtype != EC_FP32) return EC_E_INVAL;
+    if (!factor_ok(d_x, dtype, rows, cols, x_stride) || !factor_ok(d_y, out_dtype, rows, cols, y_stride))
+        return EC_E_INVAL;
+    if ((d_weight && !tensor_ok(d_weight, w_dtype, 1, cols, cols)) || (d_bias && !tensor_ok(d_bias, w_dtype, 1, cols, cols)))
+        return EC_E_INVAL;
+    if (((uintptr_t)d_out_scale | (uintptr_t)d_mean | (uintptr_t)d_rstd) & 3) return EC_E_INVAL;
+    if ((d_out_scale && out_dtype != EC_E4M3) || !(eps >= 0.0f)) return EC_E_INVAL;
+    NormArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = d_x;
+    a.rows = rows;
+    a.x_stride = x_stride;
+    a.cols = (uint32_t)cols;
+    a.dtype = dtype;
+    a.w_dtype = w_dtype;
+    a.out_dtype = out_dtype;
+    a.weight = d_weight;
+    a.bias = d_bias;
+    a.eps = eps;
+    a.y = d_y;
+    a.y_stride = y_stride;
+    a.out_scale = d_out_scale;
+    a.mean = d_mean;
+    a.rstd = d_rstd;
+    return hip_code(launch_norm(a, stream));
+}
+
+uint64_t layer_norm_grad_workspace_bytes(uint64_t rows, uint64_t cols) {
+    if (!cols || cols > 65536 || rows > kMaxSize) return 0;
+    return (uint64_t)norm_grad_parts(rows, cols) * 2 * cols * sizeof(float);
+}
+
+int layer_norm_grad(const void *d_dy, uint64_t dy_stride, const void *d_x, uint64_t x_stride, uint32_t dtype,
+                    uint64_t rows, uint64_t cols, const float *d_mean, const float *d_rstd,
+                    const void *d_weight, uint32_t w_dtype, const void *d_dres, uint64_t dres_stride, void *d_dx,
+                    uint64_t dx_stride, float *d_dweight, float *d_dbias, void *d_workspace,
+                    uint64_t workspace_bytes, hipStream_t stream) {
+    if ((dtype != EC_BF16 && dtype != EC_FP32) || !cols || cols > 65536 || rows > kMaxSize) return EC_E_INVAL;
+    if (d_weight && ((w_dtype != EC_BF16 && w_dtype != EC_FP32) || !tensor_ok(d_weight, w_dtype, 1, cols, cols)))
+        return EC_E_INVAL;
+    if (!factor_ok(d_dy, dtype, rows, cols, dy_stride) || !factor_ok(d_x, dtype, rows, cols, x_stride))
+        return EC_E_INVAL;
+    if (rows && (!d_mean || !d_rstd)) return EC_E_INVAL;
+    if (d_dres && !tensor_ok(d_dres, dtype, rows, cols, dres_stride)) return EC_E_INVAL;
+    if (d_dx && !tensor_ok(d_dx, dtype, rows, cols, dx_stride)) return EC_E_INVAL;
+    if (((uintptr_t)d_mean | (uintptr_t)d_rstd | (uintptr_t)d_dweight | (uintptr_t)d_dbias) & 3) return EC_E_INVAL;
+    if ((d_dweight || d_dbias) && (!d_workspace || ((uintptr_t)d_workspace & 15) ||
+                                   workspace_bytes < layer_norm_grad_workspace_bytes(rows, cols)))
+        return EC_E_INVAL;
+    NormGradArgs a;
+    memset(&a, 0, sizeof(a));
+    a.dy = d_dy;
+    a.x = d_x;
+    a.weight = d_weight;
+    a.dres = d_dres;
+    a.rows = rows;
+    a.dy_stride = dy_stride;
+    a.x_stride = x_stride;
+    a.dres_stride = dres_stride;
+    a.dx_stride = dx_stride;
+    a.cols = (uint32_t)cols;
+    a.dtype = dtype;
+    a.w_dtype = w_dtype;
+    a.mean = d_mean;
+    a.rstd = d_rstd;
+    a.dx = d_dx;
+    a.dweight = d_dweight;
+    a.dbias = d_dbias;
+    a.partial = (float *)d_workspace;
+    a.parts = norm_grad_parts(rows, cols);
+    return hip_code(launch_norm_grad(a, stream));
+}
