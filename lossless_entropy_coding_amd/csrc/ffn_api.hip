@@ -149,31 +149,47 @@ ProductArgs product(const ec_linear_args *a, uint32_t op) {
 
 using namespace ec;
 
+namespace {
+
+int check(const ec_linear_args *a, uint32_t op) {
+    switch (op) {
+        case EC_LINEAR_FORWARD: return check_forward(a);
+        case EC_LINEAR_GRAD_INPUT: return check_grad_input(a);
+        case EC_LINEAR_GRAD_WEIGHT: return check_grad_weight(a);
+    }
+    return EC_E_INVAL;
+}
+
+bool has_product(const ec_linear_args *a, uint32_t op) { return op != EC_LINEAR_GRAD_WEIGHT || a->d_dw; }
+
+int run_product(const ec_linear_args *a, uint32_t op, hipStream_t stream) {
+    const ProductArgs p = product(a, op);
+    const uint64_t need = product_workspace(p);
+    if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;
+    return hip_code(launch_product(p, a->d_workspace, stream));
+}
+
+}  // namespace
+
 uint64_t linear_workspace_bytes(const ec_linear_args *a, uint32_t op) {
-    (void)a;
-    (void)op;
-    return 0;
+    if (check(a, op) || !has_product(a, op)) return 0;
+    return product_workspace(product(a, op));
 }
 
 int linear_forward(const ec_linear_args *a, hipStream_t stream) {
     const int rc = check_forward(a);
-    if (rc) return rc;
-    return hip_code(launch_product(product(a, EC_LINEAR_FORWARD), stream));
+    return rc ? rc : run_product(a, EC_LINEAR_FORWARD, stream);
 }
 
 int linear_grad_input(const ec_linear_args *a, hipStream_t stream) {
     const int rc = check_grad_input(a);
-    if (rc) return rc;
-    return hip_code(launch_product(product(a, EC_LINEAR_GRAD_INPUT), stream));
+    return rc ? rc : run_product(a, EC_LINEAR_GRAD_INPUT, stream);
 }
 
 int linear_grad_weight(const ec_linear_args *a, hipStream_t stream) {
-    const int rc = check_grad_weight(a);
+    int rc = check_grad_weight(a);
     if (rc) return rc;
-    if (a->d_dw) {
-        const hipError_t e = launch_product(product(a, EC_LINEAR_GRAD_WEIGHT), stream);
-        if (e != hipSuccess) return EC_E_HIP;
-    }
+    if (a->d_dw && (rc = run_product(a, EC_LINEAR_GRAD_WEIGHT, stream))) return rc;
     if (!a->d_db) return EC_OK;
     ColumnSumArgs c;
     memset(&c, 0, sizeof(c));

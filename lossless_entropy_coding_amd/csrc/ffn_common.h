@@ -15,6 +15,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -49,6 +50,9 @@ struct ProductArgs {
     uint64_t out_stride, out_group;        // out_group: elements between experts' dw
     uint16_t *preact;                      // written (forward) or read (grad input)
     uint64_t preact_stride;
+    // filled in by the plan
+    uint32_t tiles_i, tiles_j, splits;
+    float *partial;                        // [splits][tile][TI * TJ] when splits > 1
 };
 
 struct ColumnSumArgs {                     // db
@@ -62,7 +66,8 @@ struct ColumnSumArgs {                     // db
     uint32_t *status;
 };
 
-hipError_t launch_product(const ProductArgs &a, hipStream_t s);
+uint64_t product_workspace(const ProductArgs &a);
+hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s);
 hipError_t launch_column_sum(const ColumnSumArgs &a, hipStream_t s);
 
 struct NormArgs {
@@ -106,6 +111,14 @@ __device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi) {
     b[0] = (__bf16)lo;
     b[1] = (__bf16)hi;
     return __builtin_bit_cast(uint32_t, b);
+}
+
+__device__ __forceinline__ bf16x8 e4m3_to_bf16x8(uint32_t lo, uint32_t hi) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // The conversion makes NaN of what is beyond 448; e4m3 bytes here saturate
@@ -185,59 +198,78 @@ __device__ __forceinline__ void group_range(const int32_t *offsets, uint32_t m, 
     *hi = min((uint32_t)max(before, offsets[g + 1]), m);
 }
 
+// A grouped product's rows fall into ranges: those before the first offset,
+// those of each group, and those after the last.  Each range is cut into
+// tiles of `tile` rows, in this order: at most m / tile + (ranges with rows)
+// of them.
 struct RowTile {
     uint32_t row, end;     // rows [row, end) of the group, at most one tile
     uint32_t group;
-    bool none, zero;       // past the last tile; rows of no group (written as zeros)
+    bool zero;             // rows of no group (written as zeros)
 };
 
-// Tile t of a grouped product, tiles of `tile` rows: the rows before the
-// first offset, those of each group, and those after the last, cut into tiles
-// in this order.  Tiles number at most ceil(m / tile) + groups + 2.  All 64
-// lanes of a wave call it.
+// 64 of the ranges, one a lane: [start, end), and the tiles up to and with
+// the lane's.  edge and tiles carry over from the ranges before.
+__device__ __forceinline__ void scan_ranges(const int32_t *offsets, uint32_t groups, uint32_t m, uint32_t tile,
+                                            uint32_t base, uint32_t edge, uint32_t tiles, uint32_t *start,
+                                            uint32_t *end, uint32_t *n, uint32_t *sum) {
+    const uint32_t lane = threadIdx.x & 63, r = base + lane;
+    // range r = 0 .. groups + 1 ends at offset[r] (r <= groups) or m
+    uint32_t e = r <= groups ? (uint32_t)min(max(offsets[r], 0), (int32_t)m) : m;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {      // running maximum
+        const uint32_t o = (uint32_t)__shfl_up((int)e, d);
+        if (lane >= (uint32_t)d) e = max(e, o);
+    }
+    e = max(e, edge);
+    uint32_t s = (uint32_t)__shfl_up((int)e, 1);
+    if (lane == 0) s = edge;
+    const uint32_t c = r < groups + 2 ? (e - s + tile - 1) / tile : 0;
+    uint32_t t = c;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_up((int)t, d);
+        if (lane >= (uint32_t)d) t += o;
+    }
+    *start = s;
+    *end = e;
+    *n = c;
+    *sum = t + tiles;
+}
+
+// The number of row tiles; all 64 lanes of a wave call it.
+__device__ __forceinline__ uint32_t count_row_tiles(const int32_t *offsets, uint32_t groups, uint32_t m,
+                                                    uint32_t tile) {
+    uint32_t edge = 0, tiles = 0, start, end, n, sum;
+    for (uint32_t base = 0; base < groups + 2; base += 64) {
+        scan_ranges(offsets, groups, m, tile, base, edge, tiles, &start, &end, &n, &sum);
+        edge = (uint32_t)__shfl((int)end, 63);
+        tiles = (uint32_t)__shfl((int)sum, 63);
+    }
+    return tiles;
+}
+
+// Row tile t (less than their number); all 64 lanes of a wave call it.
 __device__ __forceinline__ RowTile find_row_tile(const int32_t *offsets, uint32_t groups, uint32_t m, uint32_t tile,
                                                  uint32_t t) {
-    const uint32_t lane = threadIdx.x & 63;
-    uint32_t edge = 0, tiles = 0;          // carried: end of the ranges so far, their tiles
-    // range r = 0 .. groups + 1 ends at offset[r] (r <= groups) or m
+    uint32_t edge = 0, tiles = 0, start, end, n, sum;
+    RowTile q = {0, 0, 0, true};
     for (uint32_t base = 0; base < groups + 2; base += 64) {
-        const uint32_t r = base + lane;
-        uint32_t end = r <= groups ? (uint32_t)min(max(offsets[min(r, groups)], 0), (int32_t)m) : m;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {  // running maximum
-            const uint32_t o = (uint32_t)__shfl_up((int)end, d);
-            if (lane >= (uint32_t)d) end = max(end, o);
-        }
-        end = max(end, edge);
-        uint32_t start = (uint32_t)__shfl_up((int)end, 1);
-        if (lane == 0) start = edge;
-        uint32_t n = r < groups + 2 ? (end - start + tile - 1) / tile : 0, sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t o = (uint32_t)__shfl_up((int)sum, d);
-            if (lane >= (uint32_t)d) sum += o;
-        }
-        sum += tiles;
+        scan_ranges(offsets, groups, m, tile, base, edge, tiles, &start, &end, &n, &sum);
         const uint64_t hit = __ballot(sum > t);
         if (hit) {
             const int l = __ffsll((unsigned long long)hit) - 1;
             const uint32_t first = (uint32_t)__shfl((int)(sum - n), l);
             const uint32_t lo = (uint32_t)__shfl((int)start, l), hi = (uint32_t)__shfl((int)end, l);
-            RowTile q;
             q.row = lo + (t - first) * tile;
             q.end = min(hi, q.row + tile);
             q.zero = base + l == 0 || base + l == groups + 1;
             q.group = q.zero ? 0 : base + l - 1;
-            q.none = false;
-            return q;
+            break;
         }
         edge = (uint32_t)__shfl((int)end, 63);
         tiles = (uint32_t)__shfl((int)sum, 63);
     }
-    RowTile q;
-    q.none = true;
-    q.zero = false;
-    q.row = q.end = q.group = 0;
     return q;
 }
 
@@ -255,92 +287,159 @@ __device__ __forceinline__ void check_offsets(const int32_t *offsets, uint32_t g
 
 // ------------------------------------------------------------------- epilogue
 
-// Stores V consecutive values of output row i, columns j .. j + V - 1 (clipped
-// to J), after the epilogue of `OP`.  `zero` rows get zeros.
-template <int OP, int ACT, int V>
-__device__ __forceinline__ void store_values(const ProductArgs &p, uint32_t g, uint32_t i, uint32_t j, const float *acc,
-                                             bool zero) {
-    float v[V], z[V];
-    const uint32_t left = p.J > j ? p.J - j : 0;
-    if (!left) return;
-    const bool whole = left >= (uint32_t)V;
+// Vectors at any address that suits their elements.
+struct __attribute__((packed, aligned(2))) AnyU32x4 { u32x4 v; };
+struct __attribute__((packed, aligned(1))) AnyU32x2 { u32x2 v; };
+struct __attribute__((packed, aligned(4))) AnyF32x4 { f32x4 v; };
+
+// Eight values of bf16 or fp32 at p[at ..], of which `left` exist (the rest read as zero).
+__device__ __forceinline__ void load8_bf16(const void *p, uint64_t at, uint32_t left, float *v) {
+    const uint16_t *b = (const uint16_t *)p + at;
+    if (left >= 8) {
+        const u32x4 w = ((const AnyU32x4 *)b)->v;
 #pragma unroll
-    for (int q = 0; q < V; ++q) v[q] = acc[q];
+        for (int q = 0; q < 4; ++q) {
+            v[2 * q] = __uint_as_float(w[q] << 16);
+            v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < (int)left ? bf16_to_f32(b[q]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void load8(const void *p, uint32_t dtype, uint64_t at, uint32_t left, float *v) {
+    if (dtype == EC_BF16) {
+        load8_bf16(p, at, left, v);
+    } else if (left >= 8) {
+        const AnyF32x4 *f = (const AnyF32x4 *)((const float *)p + at);
+        const f32x4 a = f[0].v, b = f[1].v;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] = a[q];
+            v[q + 4] = b[q];
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < (int)left ? ((const float *)p)[at + q] : 0.0f;
+    }
+}
+
+// Stores eight values as `dtype`, the first `left` of them.
+__device__ __forceinline__ void store8(void *p, uint32_t dtype, uint64_t at, uint32_t left, const float *v) {
+    if (dtype == EC_BF16) {
+        uint16_t *o = (uint16_t *)p + at;
+        u32x4 w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = f32_to_bf16x2(v[2 * q], v[2 * q + 1]);
+        if (left >= 8)
+            ((AnyU32x4 *)o)->v = w;
+        else
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < (int)left) o[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
+    } else if (dtype == EC_E4M3) {
+        uint8_t *o = (uint8_t *)p + at;
+        u32x2 w;
+        w[0] = f32_to_e4m3x4(v[0], v[1], v[2], v[3]);
+        w[1] = f32_to_e4m3x4(v[4], v[5], v[6], v[7]);
+        if (left >= 8)
+            ((AnyU32x2 *)o)->v = w;
+        else
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < (int)left) o[q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
+    } else {
+        float *o = (float *)p + at;
+        if (left >= 8) {
+            ((AnyF32x4 *)o)[0].v = f32x4{v[0], v[1], v[2], v[3]};
+            ((AnyF32x4 *)o)[1].v = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < (int)left) o[q] = v[q];
+        }
+    }
+}
+
+// What the epilogue of eight output columns needs besides the sums.
+struct Columns {
+    float w_scale[8], bias[8];
+    uint32_t left;                         // columns that exist, of those from j on
+};
+
+template <int OP>
+__device__ __forceinline__ Columns load_columns(const ProductArgs &p, uint32_t g, uint32_t j) {
+    Columns c;
+    c.left = p.J > j ? p.J - j : 0;
+    if constexpr (OP == EC_LINEAR_FORWARD) {
+        if (p.w_scale) {
+            if (p.w_scales > 1) {
+                load8(p.w_scale, EC_FP32, (uint64_t)g * p.w_scales + j, c.left, c.w_scale);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) c.w_scale[q] = p.w_scale[g];
+            }
+        }
+        if (p.bias) load8(p.bias, p.bias_dtype, (uint64_t)g * p.J + j, c.left, c.bias);
+    }
+    return c;
+}
+
+// The residual (forward) or the activation's input (grad input) of eight columns of row i.
+template <int OP>
+__device__ __forceinline__ void load_side(const ProductArgs &p, uint32_t i, uint32_t j, uint32_t left, float *v) {
+    if constexpr (OP == EC_LINEAR_FORWARD) {
+        if (p.residual && left) load8_bf16(p.residual, i * p.residual_stride + j, left, v);
+    } else if constexpr (OP == EC_LINEAR_GRAD_INPUT) {
+        if (p.act != EC_ACT_NONE && left) load8_bf16(p.preact, i * p.preact_stride + j, left, v);
+    }
+}
+
+// Finishes and stores eight sums of row i, columns j .. j + 7.  `zero` rows
+// get zeros (their sums are zeros, and only the bias could make them others).
+template <int OP, int ACT>
+__device__ __forceinline__ void finish8(const ProductArgs &p, uint32_t g, uint32_t i, uint32_t j, float *v,
+                                        const Columns &c, const float *side, float x_scale, float out_scale,
+                                        bool zero) {
+    if (!c.left) return;
     if constexpr (OP == EC_LINEAR_FORWARD) {
         if (p.x_scale) {
-            const float f = p.x_scale[p.x_scales > 1 ? i : 0];
 #pragma unroll
-            for (int q = 0; q < V; ++q) v[q] *= f;
+            for (int q = 0; q < 8; ++q) v[q] *= x_scale;
         }
         if (p.w_scale) {
-            const float *f = p.w_scale + (uint64_t)g * p.w_scales;
 #pragma unroll
-            for (int q = 0; q < V; ++q) v[q] *= p.w_scales > 1 ? f[min(j + q, p.J - 1)] : f[0];
+            for (int q = 0; q < 8; ++q) v[q] *= c.w_scale[q];
         }
         if (p.bias) {
-            const uint64_t at = (uint64_t)g * p.J + j;
 #pragma unroll
-            for (int q = 0; q < V; ++q)
-                if (q < (int)left)
-                    v[q] += p.bias_dtype == EC_FP32 ? ((const float *)p.bias)[at + q]
-                                                    : bf16_to_f32(((const uint16_t *)p.bias)[at + q]);
+            for (int q = 0; q < 8; ++q) v[q] += c.bias[q];
         }
+        if (zero) {
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-            z[q] = v[q];
-            v[q] = act_value<ACT>(v[q]);
+            for (int q = 0; q < 8; ++q) v[q] = 0.0f;
         }
-        if (p.residual) {
-            const uint16_t *r = p.residual + i * p.residual_stride + j;
+        if (p.preact) store8(p.preact, EC_BF16, i * p.preact_stride + j, c.left, v);
 #pragma unroll
-            for (int q = 0; q < V; ++q)
-                if (q < (int)left) v[q] += bf16_to_f32(r[q]);
+        for (int q = 0; q < 8; ++q) v[q] = act_value<ACT>(v[q]);
+        if (p.residual && !zero) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += side[q];
         }
         if (p.out_scale) {
-            const float f = *p.out_scale;
 #pragma unroll
-            for (int q = 0; q < V; ++q) v[q] *= f;
-        }
-        if (p.preact) {
-            uint16_t *o = p.preact + i * p.preact_stride + j;
-#pragma unroll
-            for (int q = 0; q < V; ++q)
-                if (q < (int)left) o[q] = zero ? 0 : f32_to_bf16(z[q]);
+            for (int q = 0; q < 8; ++q) v[q] *= out_scale;
         }
     } else if constexpr (OP == EC_LINEAR_GRAD_INPUT) {
         if constexpr (ACT != EC_ACT_NONE) {
-            const uint16_t *r = p.preact + i * p.preact_stride + j;
+            if (!zero) {
 #pragma unroll
-            for (int q = 0; q < V; ++q)
-                if (q < (int)left) v[q] *= act_slope<ACT>(bf16_to_f32(r[q]));
+                for (int q = 0; q < 8; ++q) v[q] *= act_slope<ACT>(side[q]);
+            }
         }
     }
-    if (zero) {
-#pragma unroll
-        for (int q = 0; q < V; ++q) v[q] = 0.0f;
-    }
-    const uint64_t at = (OP == EC_LINEAR_GRAD_WEIGHT ? g * p.out_group : 0) + i * p.out_stride + j;
-    (void)whole;
-    if (p.out_dtype == EC_FP32) {
-        float *o = (float *)p.out + at;
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-            if (q < (int)left) o[q] = v[q];
-    } else if (p.out_dtype == EC_BF16) {
-        uint16_t *o = (uint16_t *)p.out + at;
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-            if (q < (int)left) o[q] = f32_to_bf16(v[q]);
-    } else {
-        uint8_t *o = (uint8_t *)p.out + at;
-#pragma unroll
-        for (int q = 0; q < V; q += 4) {
-            const uint32_t u = f32_to_e4m3x4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (q + r < (int)left) o[q + r] = (uint8_t)(u >> (8 * r));
-        }
-    }
+    store8(p.out, p.out_dtype, (OP == EC_LINEAR_GRAD_WEIGHT ? g * p.out_group : 0) + i * p.out_stride + j, c.left, v);
 }
 
 }  // namespace ec

@@ -1,86 +1,462 @@
 // Matrix products with a fused epilogue, dense and grouped by expert.
+#include <string.h>
+
 #include "ffn_common.h"
 
 namespace ec {
 namespace {
 
-// ------------------------------------------------------------ simple product
-//
-// Tiles of 64 x 64 outputs, four waves of 32 x 32 each (2 x 2 MFMA tiles of
-// 16 x 16 x 32).  The factors' tiles go through registers into LDS element by
-// element, bounds checked, so any stride and size is right; e4m3 values are
-// exact in bf16.  The j side is the MFMA's first operand, so that a lane ends
-// up with four consecutive columns of one row.
-constexpr int kTile = 64, kDepth = 32, kPitch = kDepth + 8;
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-template <bool E4M3>
-__device__ __forceinline__ __bf16 element(const void *p, uint64_t at) {
-    if constexpr (E4M3)
-        return (__bf16)__builtin_amdgcn_cvt_f32_fp8((int)((const uint8_t *)p)[at], 0);
-    else
-        return ((const __bf16 *)p)[at];
+// ------------------------------------------------------------- tiled product
+//
+// A workgroup of four waves makes a TI x TJ tile of D, WI x WJ waves side by
+// side, each a block of 32 x 32 tiles of the matrix units.  The contraction
+// is walked in stages of 64 bytes (32 bf16 or 64 e4m3 values); S stages of
+// both factors lie in LDS and are filled by loads that bypass the registers.
+// The fragments of a stage are read while the products of the one before run.
+template <int TI_, int TJ_, int WI_, int WJ_, int S_, int PER_CU_>
+struct Shape {
+    static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, S = S_, PER_CU = PER_CU_;
+    static constexpr int NI = TI / WI / 32, NJ = TJ / WJ / 32;
+    static constexpr int kStage = (TI + TJ) * 64;
+};
+
+constexpr int kStageBytes = 64;            // of the contraction
+constexpr uint32_t kOutside = 0x80000000u; // an offset past every buffer: reads as zero
+
+__device__ __forceinline__ constexpr uint32_t unit_order(uint32_t c, uint32_t T) {
+    return (2 * (c & 3) + ((c >> 1) & 1)) & (T / 16 - 1);
 }
 
-template <int OP, int ACT, bool E4M3>
-__global__ __launch_bounds__(256) void simple_product_kernel(ProductArgs p) {
-    __shared__ __attribute__((aligned(16))) __bf16 ta[kTile * kPitch], tb[kTile * kPitch];
-    uint32_t g = 0, i0 = blockIdx.y * kTile, i1 = min(p.I, i0 + kTile), c0 = 0, c1 = p.C;
-    bool zero = false;
-    if (p.groups) {
-        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 64)
-            check_offsets(p.offsets, p.groups, OP == EC_LINEAR_GRAD_WEIGHT ? p.C : p.I, p.status);
-        if (OP == EC_LINEAR_GRAD_WEIGHT) {
-            g = blockIdx.z;
-            group_range(p.offsets, p.C, g, &c0, &c1);
+// One factor's tile of T rows (i or j) by one stage.
+//
+// Rows contiguous along the contraction: the tile holds row r at r * 64, its
+// four 16-byte chunks in the order chunk ^ (r / 2 % 4), so that eight rows'
+// equal chunks cover all banks.  Contraction outermost (OUTER): the tile
+// holds stage row c at c * 2 T, its 32-byte units in the order unit ^ h(c),
+// h = 2 (c % 4) + c / 2 % 2 (modulo the units of a row), so that the four rows of a transposed read fall
+// into different banks.  A load writes 1 KB of consecutive LDS per wave; the
+// order is made by which address each lane reads.
+template <int T, bool OUTER, int ES>
+struct Factor {
+    static constexpr int kBytes = T * kStageBytes, kInstr = kBytes / 1024, kLoads = (kInstr + 3) / 4;
+    static constexpr int kDepth = kStageBytes / ES;     // contraction values a stage
+    static constexpr int kRowsPer = 1024 / (T * 2);     // OUTER: stage rows a load
+    uint32_t off[kLoads];                               // per lane
+    uint64_t base;                                      // of the stage
+    int64_t left;                                       // bytes from base to the end of what may be read
+    uint64_t step;
+
+    // rows: of the tile that exist; stride in elements; first and count along the contraction
+    __device__ __forceinline__ void init(const void *p, uint64_t stride, uint64_t row0, uint32_t rows, uint32_t c0,
+                                         uint32_t c1, uint32_t wave, uint32_t lane) {
+        const uint64_t sb = stride * ES;
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+            const uint32_t q = (n * 4 + wave) % kInstr;
+            if constexpr (OUTER) {
+                constexpr uint32_t kLane = 64 / kRowsPer;
+                const uint32_t c = q * kRowsPer + lane / kLane, pos = lane % kLane;
+                const uint32_t h = unit_order(c, T);
+                off[n] = c * (uint32_t)sb + ((((pos >> 1) ^ h) << 1) | (pos & 1)) * 16;
+            } else {
+                const uint32_t r = q * 16 + (lane >> 2);
+                off[n] = r * (uint32_t)sb + ((lane & 3) ^ ((r >> 1) & 3)) * 16;
+            }
+        }
+        if constexpr (OUTER) {
+            base = (uint64_t)p + c0 * sb + row0 * ES;
+            left = ((int64_t)(c1 - c0) - 1) * (int64_t)sb + rows * ES;
+            step = kDepth * sb;
         } else {
-            const RowTile q = find_row_tile(p.offsets, p.groups, p.I, kTile, blockIdx.y);
-            if (q.none) return;
-            g = q.group;
-            i0 = q.row;
-            i1 = q.end;
-            zero = q.zero;
-            if (zero) c1 = 0;
+            base = (uint64_t)p + row0 * sb + (uint64_t)c0 * ES;
+            left = ((int64_t)rows - 1) * (int64_t)sb + (int64_t)(c1 - c0) * ES;
+            step = kStageBytes;
+        }
+        left = (left + 3) & ~3ll;           // whole dwords: the last one holds valid elements
+    }
+
+    // Loads the next stage into LDS at `at`; `rest` is what remains of the
+    // contraction, in bytes of a row (not OUTER): chunks past it read as zero.
+    __device__ __forceinline__ void load(uint32_t at, int32_t rest, uint32_t wave, uint32_t lane) {
+        i32x4 d;
+        const int64_t n = left < 0 ? 0 : left > 0x7FFFFFFF ? 0x7FFFFFFF : left;
+        d[0] = __builtin_amdgcn_readfirstlane((int)base);
+        d[1] = __builtin_amdgcn_readfirstlane((int)(base >> 32) & 0xFFFF);
+        d[2] = __builtin_amdgcn_readfirstlane(rest > 0 ? (int)n : 0);
+        d[3] = 0x00027000;
+        uint32_t out = 0;
+        if constexpr (!OUTER) out = (int32_t)(((lane & 3) ^ ((lane >> 3) & 3)) * 16) < rest ? 0 : kOutside;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const uint32_t q = (k * 4 + wave) % kInstr;
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at + q * 1024),
+                         "v"(off[k] | out), "s"(d)
+                         : "memory");
+        }
+        base += step;
+        left -= (int64_t)step;
+    }
+};
+
+// A wave's fragments of one factor: N tiles of 32 rows by the two halves of a stage.
+template <int T, int N, bool OUTER>
+struct Fragments {
+    // per-lane LDS offsets within a stage of the factor
+    static __device__ __forceinline__ uint32_t at(uint32_t wave_row, int t, uint32_t lane) {
+        if constexpr (OUTER) {
+            const uint32_t c = 8 * (lane >> 5) + ((lane & 15) >> 2), h = unit_order(c, T);
+            const uint32_t unit = wave_row / 16 + t * 2 + ((lane >> 4) & 1);
+            return c * (2 * T) + (unit ^ h) * 32 + (lane & 3) * 8;
+        } else {
+            return (wave_row + t * 32 + (lane & 31)) * 64 + ((lane >> 5) ^ ((lane >> 1) & 3)) * 16;
         }
     }
-    const uint32_t j0 = blockIdx.x * kTile;
+
+    static __device__ __forceinline__ void read(u32x4 (&f)[N][2], lds_char *stage, const uint32_t *offs) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            if constexpr (OUTER) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    union {
+                        s16x4 h[2];
+                        u32x4 w;
+                    } u;
+                    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + offs[t] + s * 16 * 2 * T));
+                    u.h[1] =
+                        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + offs[t] + (s * 16 + 4) * 2 * T));
+                    f[t][s] = u.w;
+                }
+            } else {
+                f[t][0] = *(lds_u32x4 *)(stage + offs[0] + t * 2048);
+                f[t][1] = *(lds_u32x4 *)(stage + (offs[0] ^ 32) + t * 2048);
+            }
+        }
+    }
+};
+
+template <int NI, int NJ, bool E4M3>
+__device__ __forceinline__ void multiply(f32x16 (&acc)[NI][NJ], const u32x4 (&a)[NI][2], const u32x4 (&b)[NJ][2]) {
+    if constexpr (E4M3) {
+        // e4m3 values are exact in bf16, and the products of bf16 are added in
+        // 32 bits.  The e4m3 instructions are not used: they cut the products
+        // they add to a few bits below the largest (measured: sums of 16 off
+        // by up to 2^-14 of the sum of magnitudes, against 2^-26 here), where
+        // sums are to be held in 32 bits.
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            bf16x8 fa[NI], fb[NJ];
+#pragma unroll
+            for (int x = 0; x < NI; ++x) fa[x] = e4m3_to_bf16x8(a[x][s >> 1][2 * (s & 1)], a[x][s >> 1][2 * (s & 1) + 1]);
+#pragma unroll
+            for (int y = 0; y < NJ; ++y) fb[y] = e4m3_to_bf16x8(b[y][s >> 1][2 * (s & 1)], b[y][s >> 1][2 * (s & 1) + 1]);
+#pragma unroll
+            for (int x = 0; x < NI; ++x)
+#pragma unroll
+                for (int y = 0; y < NJ; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[y], fa[x], acc[x][y], 0, 0, 0);
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int x = 0; x < NI; ++x)
+#pragma unroll
+                for (int y = 0; y < NJ; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b[y][s]),
+                                                                        __builtin_bit_cast(bf16x8, a[x][s]), acc[x][y],
+                                                                        0, 0, 0);
+    }
+}
+
+// ----------------------------------------------------------------- epilogue
+
+// The wave's accumulators hold, of each 32 x 32 tile, row i = lane % 32 and
+// columns 8 g + 4 (lane / 32) + r in register 4 g + r.  Two halves of the
+// wave exchange registers so that a lane has eight consecutive columns.
+__device__ __forceinline__ void eight_columns(const f32x16 &c, int q, float *v) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[8 * q + r]), __float_as_uint(c[8 * q + 4 + r]),
+                                                        false, false);
+        v[r] = __uint_as_float(s[0]);
+        v[4 + r] = __uint_as_float(s[1]);
+    }
+}
+
+template <int NI, int NJ, int OP, int ACT>
+__device__ __forceinline__ void finish_tiles(const ProductArgs &p, f32x16 (&acc)[NI][NJ], uint32_t g, uint32_t i0,
+                                             uint32_t i1, uint32_t j0, bool zero) {
+    const uint32_t lane = threadIdx.x & 63;
+    float xs[NI];
+    const float os = OP == EC_LINEAR_FORWARD && p.out_scale ? *p.out_scale : 1.0f;
+#pragma unroll
+    for (int x = 0; x < NI; ++x) {
+        const uint32_t i = i0 + x * 32 + (lane & 31);
+        xs[x] = 1.0f;
+        if (OP == EC_LINEAR_FORWARD && p.x_scale && i < i1) xs[x] = p.x_scale[p.x_scales > 1 ? i : 0];
+    }
+#pragma unroll
+    for (int y = 0; y < NJ; ++y) {
+        Columns c[2];
+        float side[NI][2][8];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t j = j0 + y * 32 + q * 16 + (lane >> 5) * 8;
+            c[q] = load_columns<OP>(p, g, j);
+#pragma unroll
+            for (int x = 0; x < NI; ++x) {
+                const uint32_t i = i0 + x * 32 + (lane & 31);
+                if (i < i1) load_side<OP>(p, i, j, c[q].left, side[x][q]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < NI; ++x)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t i = i0 + x * 32 + (lane & 31), j = j0 + y * 32 + q * 16 + (lane >> 5) * 8;
+                float v[8];
+                eight_columns(acc[x][y], q, v);
+                if (i < i1) finish8<OP, ACT>(p, g, i, j, v, c[q], side[x][q], xs[x], os, zero);
+            }
+    }
+}
+
+template <int NI, int NJ, int OP>
+__device__ __forceinline__ void finish(const ProductArgs &p, f32x16 (&acc)[NI][NJ], uint32_t g, uint32_t i0,
+                                       uint32_t i1, uint32_t j0, bool zero) {
+    if constexpr (OP == EC_LINEAR_GRAD_WEIGHT) {
+        finish_tiles<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero);
+    } else {
+        switch (p.act) {
+            case EC_ACT_GELU: finish_tiles<NI, NJ, OP, EC_ACT_GELU>(p, acc, g, i0, i1, j0, zero); break;
+            case EC_ACT_SILU: finish_tiles<NI, NJ, OP, EC_ACT_SILU>(p, acc, g, i0, i1, j0, zero); break;
+            case EC_ACT_RELU: finish_tiles<NI, NJ, OP, EC_ACT_RELU>(p, acc, g, i0, i1, j0, zero); break;
+            default: finish_tiles<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero);
+        }
+    }
+}
+
+// -------------------------------------------------------------- tile order
+//
+// Workgroups go round the 8 XCDs in turn; each XCD gets a run of consecutive
+// tiles, taken in bands of kBand row tiles, the row fastest, so that what an
+// XCD works on at a time shares rows of both factors in its L2.
+constexpr uint32_t kBand = 8;
+
+__device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t total) {
+    const uint32_t x = b & 7, per = total >> 3, rem = total & 7;
+    return x * per + min(x, rem) + (b >> 3);
+}
+
+__device__ __forceinline__ void band_order(uint32_t t, uint32_t tiles_i, uint32_t tiles_j, uint32_t *ti, uint32_t *tj) {
+    const uint32_t band = t / (kBand * tiles_j), r = t - band * (kBand * tiles_j);
+    const uint32_t h = min(kBand, tiles_i - band * kBand);
+    *tj = r / h;
+    *ti = band * kBand + (r - *tj * h);
+}
+
+struct Place {
+    uint32_t i0, i1, j0, c0, c1, group, split, tile;
+    bool zero, none;
+};
+
+template <class T, int OP>
+__device__ __forceinline__ Place find_place(const ProductArgs &p, uint32_t block) {
+    Place q = {};
+    uint32_t ti, tj;
+    q.c1 = p.C;
+    if (p.groups && OP != EC_LINEAR_GRAD_WEIGHT) {
+        const uint32_t rows = (uint32_t)__builtin_amdgcn_readfirstlane(
+            (int)count_row_tiles(p.offsets, p.groups, p.I, T::TI));
+        const uint64_t total = (uint64_t)rows * p.tiles_j;
+        q.none = block >= total;
+        if (q.none) return q;
+        band_order(xcd_order(block, (uint32_t)total), rows, p.tiles_j, &ti, &tj);
+        const RowTile r = find_row_tile(p.offsets, p.groups, p.I, T::TI, ti);
+        q.i0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)r.row);
+        q.i1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)r.end);
+        q.group = (uint32_t)__builtin_amdgcn_readfirstlane((int)r.group);
+        q.zero = __builtin_amdgcn_readfirstlane((int)r.zero);
+        if (q.zero) q.c1 = 0;
+    } else {
+        const uint32_t tiles = p.tiles_i * p.tiles_j, t = xcd_order(block, gridDim.x);
+        const uint32_t z = t / tiles;
+        q.tile = t - z * tiles;
+        band_order(q.tile, p.tiles_i, p.tiles_j, &ti, &tj);
+        q.i0 = ti * T::TI;
+        q.i1 = min(p.I, q.i0 + T::TI);
+        if (p.groups) {
+            q.group = z;
+            group_range(p.offsets, p.C, z, &q.c0, &q.c1);
+            q.c0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)q.c0);
+            q.c1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)q.c1);
+        } else {
+            q.split = z;
+        }
+    }
+    q.j0 = tj * T::TJ;
+    return q;
+}
+
+template <class T, int OP, bool E4M3>
+__global__ __launch_bounds__(256, T::PER_CU) void product_kernel(ProductArgs p) {
+    constexpr bool kOuterA = OP == EC_LINEAR_GRAD_WEIGHT, kOuterB = OP != EC_LINEAR_FORWARD;
+    constexpr int kES = E4M3 ? 1 : 2, kDepth = kStageBytes / kES;
+    constexpr int NI = T::NI, NJ = T::NJ, S = T::S;
+    using FA = Factor<T::TI, kOuterA, kES>;
+    using FB = Factor<T::TJ, kOuterB, kES>;
+    using RA = Fragments<T::TI, NI, kOuterA>;
+    using RB = Fragments<T::TJ, NJ, kOuterB>;
+    __shared__ __attribute__((aligned(1024))) char lds[S * T::kStage];
+
+    if (p.groups && blockIdx.x == 0 && threadIdx.x < 64)
+        check_offsets(p.offsets, p.groups, OP == EC_LINEAR_GRAD_WEIGHT ? p.C : p.I, p.status);
+    const Place q = find_place<T, OP>(p, blockIdx.x);
+    if (q.none) return;
+    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t wi = wave / T::WJ * (NI * 32), wj = wave % T::WJ * (NJ * 32);
+
+    // the split's range of stages
+    uint32_t c0 = q.c0, c1 = q.c1;
+    if (p.splits > 1) {
+        const uint32_t stages = (c1 + kDepth - 1) / kDepth;
+        c0 = (uint32_t)((uint64_t)stages * q.split / p.splits) * kDepth;
+        c1 = min(c1, (uint32_t)((uint64_t)stages * (q.split + 1) / p.splits) * kDepth);
+    }
+    f32x16 acc[NI][NJ];
+#pragma unroll
+    for (int x = 0; x < NI; ++x)
+#pragma unroll
+        for (int y = 0; y < NJ; ++y)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[x][y][r] = 0.0f;
+
+    if (c1 > c0) {
+        const uint32_t n = (c1 - c0 + kDepth - 1) / kDepth;
+        const void *a = p.a;
+        const void *b = (const char *)p.b + (OP == EC_LINEAR_GRAD_WEIGHT ? 0 : q.group * p.b_group * kES);
+        FA fa;
+        FB fb;
+        fa.init(a, kOuterA ? p.a_c : p.a_i, q.i0, q.i1 - q.i0, c0, c1, wave, lane);
+        fb.init(b, kOuterB ? p.b_c : p.b_j, q.j0, min((uint32_t)T::TJ, p.J - q.j0), c0, c1, wave, lane);
+        lds_char *const mem = (lds_char *)lds;
+        const uint32_t mem_at = (uint32_t)(uintptr_t)mem;
+        int32_t rest = (int32_t)((c1 - c0) * kES > 0x7FFFFFFFu ? 0x7FFFFFFF : (c1 - c0) * kES);
+        uint32_t ao[NI], bo[NJ];
+#pragma unroll
+        for (int x = 0; x < NI; ++x) ao[x] = RA::at(wi, x, lane);
+#pragma unroll
+        for (int y = 0; y < NJ; ++y) bo[y] = T::TI * kStageBytes + RB::at(wj, y, lane);
+
+        const auto fill = [&](uint32_t stage) {
+            const uint32_t at = mem_at + stage * T::kStage;
+            fa.load(at, rest, wave, lane);
+            fb.load(at + FA::kBytes, rest, wave, lane);
+            rest -= kStageBytes;
+        };
+        constexpr int kLoads = FA::kLoads + FB::kLoads;
+        u32x4 af[2][NI][2], bf[2][NJ][2];
+        uint32_t fill_at = 0, read_at = 0;
+#pragma unroll
+        for (int s = 0; s < S; ++s) fill(s);
+        // stage 0 has arrived, everywhere
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * kLoads) : "memory");
+        __builtin_amdgcn_s_barrier();
+        RA::read(af[0], mem, ao);
+        RB::read(bf[0], mem, bo);
+        // Stage k: its fragments are in registers (or on the way); once every
+        // wave has them, its LDS takes stage k + S, and stage k + 1 is read.
+        const auto step = [&](int now) {
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * kLoads) : "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            fill(fill_at);
+            fill_at = fill_at + 1 == S ? 0 : fill_at + 1;
+            read_at = read_at + 1 == S ? 0 : read_at + 1;
+            RA::read(af[1 - now], mem + read_at * T::kStage, ao);
+            RB::read(bf[1 - now], mem + read_at * T::kStage, bo);
+            multiply<NI, NJ, E4M3>(acc, af[now], bf[now]);
+        };
+        for (uint32_t k = 0;;) {
+            step(0);
+            if (++k >= n) break;
+            step(1);
+            if (++k >= n) break;
+        }
+        // nothing is left in flight into this workgroup's LDS
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+
+    if (p.splits > 1) {
+        float *o = p.partial + ((uint64_t)q.split * (p.tiles_i * p.tiles_j) + q.tile) * (T::TI * T::TJ);
+        o += wave * (NI * NJ * 1024) + lane * 4;
+#pragma unroll
+        for (int x = 0; x < NI; ++x)
+#pragma unroll
+            for (int y = 0; y < NJ; ++y)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const f32x4 v = {acc[x][y][4 * r], acc[x][y][4 * r + 1], acc[x][y][4 * r + 2], acc[x][y][4 * r + 3]};
+                    *(f32x4 *)(o + ((x * NJ + y) * 4 + r) * 256) = v;
+                }
+        return;
+    }
+    finish<NI, NJ, OP>(p, acc, q.group, q.i0 + wi, q.i1, q.j0 + wj, q.zero);
+}
+
+// Adds the splits' sums in their order and finishes: a workgroup takes one
+// 32 x 32 tile of each of the four waves of a tile.
+template <class T, int OP>
+__global__ __launch_bounds__(256) void join_kernel(ProductArgs p) {
+    constexpr int NI = T::NI, NJ = T::NJ;
+    const uint32_t tile = blockIdx.x / (NI * NJ), xy = blockIdx.x - tile * (NI * NJ), x = xy / NJ, y = xy - x * NJ;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t wi = (wave >> 1) * 32, wj = (wave & 1) * 32;
-    f32x4 acc[2][2] = {};
-    const uint64_t b_at = g * p.b_group;
-    for (uint32_t c = c0; c < c1; c += kDepth) {
-        __syncthreads();
-        for (uint32_t q = threadIdx.x; q < kTile * kDepth; q += 256) {
-            const uint32_t row = q / kDepth, col = q % kDepth;
-            const bool in = c + col < c1;
-            ta[row * kPitch + col] = in && i0 + row < i1
-                                         ? element<E4M3>(p.a, (uint64_t)(i0 + row) * p.a_i + (uint64_t)(c + col) * p.a_c)
-                                         : (__bf16)0.0f;
-            tb[row * kPitch + col] = in && j0 + row < p.J
-                                         ? element<E4M3>(p.b, b_at + (uint64_t)(j0 + row) * p.b_j +
-                                                                  (uint64_t)(c + col) * p.b_c)
-                                         : (__bf16)0.0f;
+    const uint64_t tiles = (uint64_t)p.tiles_i * p.tiles_j;
+    uint32_t ti, tj;
+    band_order(tile, p.tiles_i, p.tiles_j, &ti, &tj);
+    f32x16 acc[1][1] = {};
+    const float *o = p.partial + (uint64_t)tile * (T::TI * T::TJ) + wave * (NI * NJ * 1024) + xy * 1024 + lane * 4;
+    for (uint32_t s = 0; s < p.splits; ++s, o += tiles * (T::TI * T::TJ))
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const f32x4 v = *(const f32x4 *)(o + r * 256);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[0][0][4 * r + k] += v[k];
         }
-        __syncthreads();
-        bf16x8 fa[2], fb[2];
+    const uint32_t i0 = ti * T::TI, wi = wave / T::WJ * (NI * 32) + x * 32, wj = wave % T::WJ * (NJ * 32) + y * 32;
+    finish<1, 1, OP>(p, acc, 0, i0 + wi, min(p.I, i0 + T::TI), tj * T::TJ + wj, false);
+}
+
+// ------------------------------------------------------- rows made readable
+//
+// The loads above take rows at 16-byte addresses whose contraction is a whole
+// number of 16-byte chunks.  Any other factor is copied first: rows padded
+// with zeros to 16 bytes, one after the other.
+template <typename E>
+__global__ __launch_bounds__(256) void copy_rows_kernel(const E *p, uint64_t stride, uint64_t group_stride,
+                                                        uint32_t rows, uint32_t cols, E *out, uint32_t pitch) {
+    constexpr uint32_t V = 16 / sizeof(E);
+    const uint32_t chunks = pitch / V;
+    const uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint64_t row = q / chunks;
+    if (row >= rows) return;
+    const uint32_t c = (uint32_t)(q - row * chunks) * V;
+    const E *in = p + blockIdx.y * group_stride + row * stride + c;
+    union {
+        E e[V];
+        u32x4 w;
+    } u;
+    u.w = u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            fa[t] = *(const bf16x8 *)&ta[(wi + t * 16 + (lane & 15)) * kPitch + (lane >> 4) * 8];
-            fb[t] = *(const bf16x8 *)&tb[(wj + t * 16 + (lane & 15)) * kPitch + (lane >> 4) * 8];
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[y], fa[x], acc[x][y], 0, 0, 0);
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const uint32_t i = i0 + wi + x * 16 + (lane & 15), j = j0 + wj + y * 16 + (lane >> 4) * 4;
-            float v[4] = {acc[x][y][0], acc[x][y][1], acc[x][y][2], acc[x][y][3]};
-            if (i < i1) store_values<OP, ACT, 4>(p, g, i, j, v, zero);
-        }
+    for (uint32_t k = 0; k < V; ++k)
+        if (c + k < cols) u.e[k] = in[k];
+    *(u32x4 *)(out + ((uint64_t)blockIdx.y * rows + row) * pitch + c) = u.w;
 }
 
 // ---------------------------------------------------------------- column sums
@@ -97,38 +473,152 @@ __global__ __launch_bounds__(256) void column_sum_kernel(ColumnSumArgs p) {
     p.db[(uint64_t)g * p.n + n] = s;
 }
 
-template <int OP, int ACT>
-void launch_simple(const ProductArgs &a, dim3 grid, hipStream_t s) {
-    if (OP == EC_LINEAR_FORWARD && a.dtype == EC_E4M3)
-        simple_product_kernel<OP, ACT, true><<<grid, 256, 0, s>>>(a);
-    else
-        simple_product_kernel<OP, ACT, false><<<grid, 256, 0, s>>>(a);
+// ---------------------------------------------------------------------- plan
+
+using Wide = Shape<128, 256, 2, 2, 3, 2>;
+using Even = Shape<128, 128, 2, 2, 4, 2>;
+using Small = Shape<64, 64, 2, 2, 6, 2>;
+using Flat = Shape<32, 128, 1, 4, 6, 2>;
+
+enum ShapeId { kWide, kEven, kSmall, kFlat };
+constexpr uint32_t kTI[] = {128, 128, 64, 32}, kTJ[] = {256, 128, 64, 128};
+
+struct Plan {
+    uint32_t shape, splits, tiles_i, tiles_j;
+    uint64_t blocks;
+    uint32_t a_pitch, b_pitch;              // elements; 0: read in place
+    uint64_t a_at, b_at, partial_at, bytes; // workspace
+};
+
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+uint64_t round_up(uint64_t a, uint64_t b) { return ceil_div(a, b) * b; }
+
+bool readable(const void *p, uint64_t stride, uint64_t group, uint64_t cols, uint32_t es, bool outer) {
+    if (((uintptr_t)p | (stride * es) | (group * es)) & 15) return false;
+    if (!outer && (cols * es & 15)) return false;
+    return 256 * stride * es + 65536 < (1ull << 31); // a tile's offsets fit 31 bits
 }
 
-template <int OP>
-void launch_act(const ProductArgs &a, dim3 grid, hipStream_t s) {
-    switch (a.act) {
-        case EC_ACT_GELU: launch_simple<OP, EC_ACT_GELU>(a, grid, s); break;
-        case EC_ACT_SILU: launch_simple<OP, EC_ACT_SILU>(a, grid, s); break;
-        case EC_ACT_RELU: launch_simple<OP, EC_ACT_RELU>(a, grid, s); break;
-        default: launch_simple<OP, EC_ACT_NONE>(a, grid, s);
+Plan make_plan(const ProductArgs &a) {
+    Plan q;
+    memset(&q, 0, sizeof(q));
+    const uint32_t es = a.dtype == EC_E4M3 ? 1 : 2;
+    const bool outer_a = a.op == EC_LINEAR_GRAD_WEIGHT, outer_b = a.op != EC_LINEAR_FORWARD;
+    const bool ragged = a.groups && !outer_a;
+    const uint64_t groups = a.groups ? a.groups : 1;
+    uint64_t at = 0;
+    if (a.C) {
+        const uint64_t a_rows = outer_a ? a.C : a.I, a_cols = outer_a ? a.I : a.C;
+        const uint64_t b_rows = outer_b ? a.C : a.J, b_cols = outer_b ? a.J : a.C;
+        if (!readable(a.a, outer_a ? a.a_c : a.a_i, 0, a_cols, es, outer_a)) {
+            q.a_pitch = (uint32_t)round_up(a_cols, 16 / es);
+            at += round_up(a_rows * q.a_pitch * es, 256);
+        }
+        q.b_at = at;
+        if (!readable(a.b, outer_b ? a.b_c : a.b_j, outer_a ? 0 : a.b_group, b_cols, es, outer_b)) {
+            q.b_pitch = (uint32_t)round_up(b_cols, 16 / es);
+            at += round_up((outer_a ? 1 : groups) * b_rows * q.b_pitch * es, 256);
+        }
     }
+    const uint64_t rows = ragged ? ceil_div(a.I, groups) : a.I; // typical of a row range
+    const uint64_t wide = ceil_div(rows, 128) * ceil_div(a.J, 256) * groups;
+    q.shape = rows <= 32 ? kFlat : wide >= 256 ? kWide : ceil_div(rows, 128) * ceil_div(a.J, 128) * groups >= 128 ? kEven : kSmall;
+    const uint32_t TI = kTI[q.shape], TJ = kTJ[q.shape];
+    uint64_t ti = ceil_div(a.I, TI);
+    if (ragged) ti = a.I / TI + (a.I < groups + 2 ? a.I : groups + 2);
+    q.tiles_i = (uint32_t)ti;
+    q.tiles_j = (uint32_t)ceil_div(a.J, TJ);
+    q.splits = 1;
+    q.blocks = ti * q.tiles_j * (outer_a ? groups : 1);
+    if (!a.groups) {
+        const uint64_t stages = ceil_div((uint64_t)a.C * es, kStageBytes);
+        uint64_t s = q.blocks ? 512 / q.blocks : 1;
+        if (s > stages / 8) s = stages / 8;
+        if (s > 32) s = 32;
+        if (s > 1) q.splits = (uint32_t)s;
+    }
+    q.partial_at = at;
+    if (q.splits > 1) {
+        at += q.splits * q.blocks * TI * TJ * 4;
+        q.blocks *= q.splits;
+    }
+    q.bytes = at;
+    return q;
+}
+
+template <class T, int OP, bool E4M3>
+void launch_shape(const ProductArgs &a, const Plan &q, hipStream_t s) {
+    product_kernel<T, OP, E4M3><<<(uint32_t)q.blocks, 256, 0, s>>>(a);
+    if (q.splits > 1) join_kernel<T, OP><<<q.tiles_i * q.tiles_j * T::NI * T::NJ, 256, 0, s>>>(a);
+}
+
+template <class T>
+void launch_op(const ProductArgs &a, const Plan &q, hipStream_t s) {
+    if (a.op == EC_LINEAR_GRAD_INPUT)
+        launch_shape<T, EC_LINEAR_GRAD_INPUT, false>(a, q, s);
+    else if (a.op == EC_LINEAR_GRAD_WEIGHT)
+        launch_shape<T, EC_LINEAR_GRAD_WEIGHT, false>(a, q, s);
+    else if (a.dtype == EC_E4M3)
+        launch_shape<T, EC_LINEAR_FORWARD, true>(a, q, s);
+    else
+        launch_shape<T, EC_LINEAR_FORWARD, false>(a, q, s);
+}
+
+hipError_t copy_rows(const void *p, uint64_t stride, uint64_t group_stride, uint64_t groups, uint64_t rows,
+                     uint64_t cols, uint32_t es, void *out, uint32_t pitch, hipStream_t s) {
+    if (!rows || !cols) return hipSuccess;
+    const uint64_t blocks = ceil_div(rows * (pitch * es / 16), 256);
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const dim3 grid((uint32_t)blocks, (uint32_t)groups);
+    if (es == 1)
+        copy_rows_kernel<uint8_t><<<grid, 256, 0, s>>>((const uint8_t *)p, stride, group_stride, (uint32_t)rows,
+                                                       (uint32_t)cols, (uint8_t *)out, pitch);
+    else
+        copy_rows_kernel<uint16_t><<<grid, 256, 0, s>>>((const uint16_t *)p, stride, group_stride, (uint32_t)rows,
+                                                        (uint32_t)cols, (uint16_t *)out, pitch);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_product(const ProductArgs &a, hipStream_t s) {
+uint64_t product_workspace(const ProductArgs &a) {
+    if (!a.I || !a.J) return 0;
+    return make_plan(a).bytes;
+}
+
+hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s) {
     if (!a.I || !a.J) return hipSuccess;
-    const bool ragged_rows = a.groups && a.op != EC_LINEAR_GRAD_WEIGHT;
-    const uint64_t row_tiles = (a.I + (uint64_t)kTile - 1) / kTile + (ragged_rows ? a.groups + 2 : 0);
-    if (row_tiles > 65535) return hipErrorInvalidValue;
-    dim3 grid((a.J + kTile - 1) / kTile, (uint32_t)row_tiles, a.op == EC_LINEAR_GRAD_WEIGHT && a.groups ? a.groups : 1);
-    if (a.op == EC_LINEAR_FORWARD)
-        launch_act<EC_LINEAR_FORWARD>(a, grid, s);
-    else if (a.op == EC_LINEAR_GRAD_INPUT)
-        launch_act<EC_LINEAR_GRAD_INPUT>(a, grid, s);
-    else
-        launch_simple<EC_LINEAR_GRAD_WEIGHT, EC_ACT_NONE>(a, grid, s);
+    const Plan q = make_plan(a);
+    if (q.blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const uint32_t es = a.dtype == EC_E4M3 ? 1 : 2;
+    const bool outer_a = a.op == EC_LINEAR_GRAD_WEIGHT, outer_b = a.op != EC_LINEAR_FORWARD;
+    char *ws = (char *)workspace;
+    if (q.a_pitch) {
+        const uint64_t rows = outer_a ? a.C : a.I, cols = outer_a ? a.I : a.C;
+        const hipError_t e = copy_rows(a.a, outer_a ? a.a_c : a.a_i, 0, 1, rows, cols, es, ws + q.a_at, q.a_pitch, s);
+        if (e != hipSuccess) return e;
+        a.a = ws + q.a_at;
+        (outer_a ? a.a_c : a.a_i) = q.a_pitch;
+    }
+    if (q.b_pitch) {
+        const uint64_t rows = outer_b ? a.C : a.J, cols = outer_b ? a.J : a.C, groups = !outer_a && a.groups ? a.groups : 1;
+        const hipError_t e =
+            copy_rows(a.b, outer_b ? a.b_c : a.b_j, a.b_group, groups, rows, cols, es, ws + q.b_at, q.b_pitch, s);
+        if (e != hipSuccess) return e;
+        a.b = ws + q.b_at;
+        (outer_b ? a.b_c : a.b_j) = q.b_pitch;
+        a.b_group = rows * q.b_pitch;
+    }
+    a.tiles_i = q.tiles_i;
+    a.tiles_j = q.tiles_j;
+    a.splits = q.splits;
+    a.partial = (float *)(ws + q.partial_at);
+    switch (q.shape) {
+        case kWide: launch_op<Wide>(a, q, s); break;
+        case kEven: launch_op<Even>(a, q, s); break;
+        case kSmall: launch_op<Small>(a, q, s); break;
+        default: launch_op<Flat>(a, q, s);
+    }
     return hipGetLastError();
 }
 
