@@ -162,6 +162,20 @@ int check(const ec_linear_args *a, uint32_t op) {
 
 bool has_product(const ec_linear_args *a, uint32_t op) { return op != EC_LINEAR_GRAD_WEIGHT || a->d_dw; }
 
+ColumnSumArgs column_sum(const ec_linear_args *a) {
+    ColumnSumArgs c;
+    memset(&c, 0, sizeof(c));
+    c.dy = (const uint16_t *)a->d_dy;
+    c.dy_stride = a->dy_stride;
+    c.m = (uint32_t)a->m;
+    c.n = (uint32_t)a->n;
+    c.groups = a->groups;
+    c.offsets = a->d_offsets;
+    c.db = a->d_db;
+    c.status = a->d_dw ? nullptr : a->d_status;     // the product reports bad offsets
+    return c;
+}
+
 int run_product(const ec_linear_args *a, uint32_t op, hipStream_t stream) {
     const ProductArgs p = product(a, op);
     const uint64_t need = product_workspace(p);
@@ -172,8 +186,13 @@ int run_product(const ec_linear_args *a, uint32_t op, hipStream_t stream) {
 }  // namespace
 
 uint64_t linear_workspace_bytes(const ec_linear_args *a, uint32_t op) {
-    if (check(a, op) || !has_product(a, op)) return 0;
-    return product_workspace(product(a, op));
+    if (check(a, op)) return 0;
+    uint64_t need = has_product(a, op) ? product_workspace(product(a, op)) : 0;
+    if (op == EC_LINEAR_GRAD_WEIGHT && a->d_db) {   // one after the other, in the same memory
+        const uint64_t sums = column_sum_workspace(column_sum(a));
+        need = sums > need ? sums : need;
+    }
+    return need;
 }
 
 int linear_forward(const ec_linear_args *a, hipStream_t stream) {
@@ -191,18 +210,10 @@ int linear_grad_weight(const ec_linear_args *a, hipStream_t stream) {
     if (rc) return rc;
     if (a->d_dw && (rc = run_product(a, EC_LINEAR_GRAD_WEIGHT, stream))) return rc;
     if (!a->d_db) return EC_OK;
-    ColumnSumArgs c;
-    memset(&c, 0, sizeof(c));
-    c.dy = (const uint16_t *)a->d_dy;
-    c.dy_stride = a->dy_stride;
-    c.m = (uint32_t)a->m;
-    c.n = (uint32_t)a->n;
-    c.groups = a->groups;
-    c.offsets = a->d_offsets;
-    c.db = a->d_db;
-    c.parts = 1;
-    c.status = a->d_status;
-    return hip_code(launch_column_sum(c, stream));
+    const ColumnSumArgs c = column_sum(a);
+    const uint64_t need = column_sum_workspace(c);
+    if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;
+    return hip_code(launch_column_sum(c, (float *)a->d_workspace, stream));
 }
 
 int layer_norm_forward(const void *d_x, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_stride,
@@ -279,7 +290,7 @@ int layer_norm_grad(const void *d_dy, uint64_t dy_stride, const void *d_x, uint6
     a.dx = d_dx;
     a.dweight = d_dweight;
     a.dbias = d_dbias;
-    a.partial = (float *)d_workspace;
+    a.partial = d_dweight || d_dbias ? (float *)d_workspace : nullptr;
     a.parts = norm_grad_parts(rows, cols);
     return hip_code(launch_norm_grad(a, stream));
 }

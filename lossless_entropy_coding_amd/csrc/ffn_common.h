@@ -61,14 +61,13 @@ struct ColumnSumArgs {                     // db
     uint32_t m, n, groups;
     const int32_t *offsets;
     float *db;
-    float *partial;                        // [parts][groups or 1][n] when parts > 1
-    uint32_t parts;
     uint32_t *status;
 };
 
 uint64_t product_workspace(const ProductArgs &a);
 hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s);
-hipError_t launch_column_sum(const ColumnSumArgs &a, hipStream_t s);
+uint64_t column_sum_workspace(const ColumnSumArgs &a);
+hipError_t launch_column_sum(const ColumnSumArgs &a, float *workspace, hipStream_t s);
 
 struct NormArgs {
     const void *x;

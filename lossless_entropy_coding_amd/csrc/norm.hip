@@ -4,143 +4,321 @@
 namespace ec {
 namespace {
 
-template <bool F32>
-__device__ __forceinline__ float load(const void *p, uint64_t at) {
-    if constexpr (F32)
-        return ((const float *)p)[at];
+// A row is held in the registers of THREADS threads, V chunks of eight
+// neighbouring values each (chunk v of thread t starts at column
+// 8 (v THREADS + t)), so x is read once and the variance is that of the
+// centred values.  Both passes are bound by the bytes they move.
+//
+// WHOLE: the columns are a multiple of eight, so a chunk is whole or empty.
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t left_of(uint32_t cols, uint32_t c) {
+    if constexpr (WHOLE)
+        return cols > c ? 8 : 0;
     else
-        return bf16_to_f32(((const uint16_t *)p)[at]);
+        return cols > c ? cols - c : 0;
 }
 
-__device__ __forceinline__ float load_w(const void *p, uint32_t dtype, uint32_t c, float none) {
-    if (!p) return none;
-    return dtype == EC_FP32 ? ((const float *)p)[c] : bf16_to_f32(((const uint16_t *)p)[c]);
-}
-
-// Sum over the workgroup's 256 threads, the same value in every thread.
-__device__ __forceinline__ float block_sum(float v, float *sh) {
+// Zeros where nothing is left.
+template <bool WHOLE>
+__device__ __forceinline__ void load_chunk(const void *p, uint32_t dtype, uint64_t at, uint32_t left, float *v) {
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return sh[0] + sh[1] + sh[2] + sh[3];
-}
-
-// One workgroup a row; the row is read three times (mean, variance, values).
-template <bool F32>
-__global__ __launch_bounds__(256) void norm_kernel(NormArgs p) {
-    __shared__ float sh[4];
-    const uint64_t row = blockIdx.x, at = row * p.x_stride;
-    float s = 0.0f;
-    for (uint32_t c = threadIdx.x; c < p.cols; c += 256) s += load<F32>(p.x, at + c);
-    const float mean = block_sum(s, sh) / p.cols;
-    s = 0.0f;
-    for (uint32_t c = threadIdx.x; c < p.cols; c += 256) {
-        const float d = load<F32>(p.x, at + c) - mean;
-        s += d * d;
-    }
-    const float rstd = 1.0f / sqrtf(block_sum(s, sh) / p.cols + p.eps);
-    if (threadIdx.x == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-    const float scale = p.out_scale ? *p.out_scale : 1.0f;
-    for (uint32_t c = threadIdx.x; c < p.cols; c += 256) {
-        const float v = (load<F32>(p.x, at + c) - mean) * rstd * load_w(p.weight, p.w_dtype, c, 1.0f) +
-                        load_w(p.bias, p.w_dtype, c, 0.0f);
-        const uint64_t o = row * p.y_stride + c;
-        if (p.out_dtype == EC_FP32)
-            ((float *)p.y)[o] = v;
-        else if (p.out_dtype == EC_BF16)
-            ((uint16_t *)p.y)[o] = f32_to_bf16(v);
-        else
-            ((uint8_t *)p.y)[o] = (uint8_t)f32_to_e4m3x4(v * scale, 0.0f, 0.0f, 0.0f);
+        for (int q = 0; q < 8; ++q) v[q] = 0.0f;
+        if (left) load8(p, dtype, at, 8, v);
+    } else {
+        load8(p, dtype, at, left, v);
     }
 }
 
-template <bool F32>
-__global__ __launch_bounds__(256) void norm_grad_kernel(NormGradArgs p) {
-    __shared__ float sh[4];
-    const uint64_t row = blockIdx.x;
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float s = 0.0f, sh_ = 0.0f;
-    for (uint32_t c = threadIdx.x; c < p.cols; c += 256) {
-        const float h = (load<F32>(p.x, row * p.x_stride + c) - mean) * rstd;
-        const float t = load<F32>(p.dy, row * p.dy_stride + c) * load_w(p.weight, p.w_dtype, c, 1.0f);
-        s += t;
-        sh_ += t * h;
-    }
-    const float mt = block_sum(s, sh) / p.cols, mth = block_sum(sh_, sh) / p.cols;
-    for (uint32_t c = threadIdx.x; c < p.cols; c += 256) {
-        const float h = (load<F32>(p.x, row * p.x_stride + c) - mean) * rstd;
-        const float t = load<F32>(p.dy, row * p.dy_stride + c) * load_w(p.weight, p.w_dtype, c, 1.0f);
-        float v = rstd * (t - mt - h * mth);
-        if (p.dres) v += load<F32>(p.dres, row * p.dres_stride + c);
-        const uint64_t o = row * p.dx_stride + c;
-        if constexpr (F32)
-            ((float *)p.dx)[o] = v;
-        else
-            ((uint16_t *)p.dx)[o] = f32_to_bf16(v);
+// weight or bias; `none` where there is none
+template <bool WHOLE>
+__device__ __forceinline__ void load_param(const void *p, uint32_t dtype, uint32_t c, uint32_t left, float none,
+                                           float *v) {
+    if (p) {
+        load_chunk<WHOLE>(p, dtype, c, left, v);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = none;
     }
 }
 
-// Partial sums of dweight and dbias over a range of rows: one thread a column.
-template <bool F32>
-__global__ __launch_bounds__(256) void norm_grad_weight_kernel(NormGradArgs p) {
-    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= p.cols) return;
-    const uint64_t per = (p.rows + p.parts - 1) / p.parts, lo = blockIdx.y * per, hi = min(p.rows, lo + per);
-    float dw = 0.0f, db = 0.0f;
-    for (uint64_t r = lo; r < hi; ++r) {
-        const float dy = load<F32>(p.dy, r * p.dy_stride + c);
-        dw += dy * (load<F32>(p.x, r * p.x_stride + c) - p.mean[r]) * p.rstd[r];
-        db += dy;
+// Sums over a row's threads, the same value in every one of them.  Every
+// thread of the workgroup calls it where a row has more than one wave.
+template <int THREADS, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float *sh) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], d);
+    if constexpr (THREADS > 64) {
+        constexpr int kWaves = THREADS / 64;
+        const uint32_t wave = threadIdx.x >> 6, first = wave / kWaves * kWaves;
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int n = 0; n < N; ++n) sh[n * 16 + wave] = v[n];
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) s += sh[n * 16 + first + w];
+            v[n] = s;
+        }
     }
-    p.partial[((uint64_t)blockIdx.y * 2) * p.cols + c] = dw;
-    p.partial[((uint64_t)blockIdx.y * 2 + 1) * p.cols + c] = db;
 }
 
+template <bool F32, bool WHOLE, int BLOCK, int THREADS, int V>
+__global__ __launch_bounds__(BLOCK) void norm_kernel(NormArgs p) {
+    constexpr int kRows = BLOCK / THREADS;                          // a workgroup's rows at a time
+    constexpr uint32_t kType = F32 ? EC_FP32 : EC_BF16;
+    __shared__ float sh[16];
+    const uint32_t t = threadIdx.x % THREADS;
+    const float scale = p.out_scale ? *p.out_scale : 1.0f, cols = (float)p.cols;
+    for (uint64_t first = (uint64_t)blockIdx.x * kRows; first < p.rows; first += (uint64_t)gridDim.x * kRows) {
+        const uint64_t row = first + threadIdx.x / THREADS;
+        const bool in = row < p.rows;
+        float x[V][8], s[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t c = 8 * (v * THREADS + t);
+            load_chunk<WHOLE>(p.x, kType, row * p.x_stride + c, in ? left_of<WHOLE>(p.cols, c) : 0, x[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s[0] += x[v][q];
+        row_sum<THREADS>(s, sh);
+        const float mean = s[0] / cols;                             // a constant row's mean is its value
+        s[0] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t left = left_of<WHOLE>(p.cols, 8 * (v * THREADS + t));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                x[v][q] -= mean;
+                s[0] += q < (int)left ? x[v][q] * x[v][q] : 0.0f;
+            }
+        }
+        row_sum<THREADS>(s, sh);
+        const float rstd = 1.0f / sqrtf(s[0] / cols + p.eps);
+        if (!in) continue;
+        if (t == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t c = 8 * (v * THREADS + t), left = left_of<WHOLE>(p.cols, c);
+            if (!left) break;
+            float w[8], b[8];
+            load_param<WHOLE>(p.weight, p.w_dtype, c, left, 1.0f, w);
+            load_param<WHOLE>(p.bias, p.w_dtype, c, left, 0.0f, b);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[v][q] = (x[v][q] * rstd * w[q] + b[q]) * scale;
+            store8(p.y, p.out_dtype, row * p.y_stride + c, left, x[v]);
+        }
+    }
+}
+
+// Backward.  A workgroup walks over rows and keeps the sums of dweight and
+// dbias for its columns in registers; they are joined over its rows in LDS
+// and written once.  Rows wider than THREADS * V * 8 are cut into slices
+// (blockIdx.y): each slice's workgroup sums over the whole row, but writes dx
+// and the sums of its own columns only.
+template <bool F32, bool WHOLE, int THREADS, int V>
+__global__ __launch_bounds__(512) void norm_grad_kernel(NormGradArgs p) {
+    constexpr int kRows = 512 / THREADS, kSlice = THREADS * V * 8;
+    constexpr uint32_t kType = F32 ? EC_FP32 : EC_BF16;
+    __shared__ float sh[32];
+    __shared__ float join[kRows > 1 ? 2 * kSlice : 1];
+    const uint32_t t = threadIdx.x % THREADS, r0 = threadIdx.x / THREADS, first = blockIdx.y * kSlice;
+    const float cols = (float)p.cols;
+    float dw[V][8] = {}, db[V][8] = {}, w[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const uint32_t c = first + 8 * (v * THREADS + t);
+        load_param<WHOLE>(p.weight, p.w_dtype, c, left_of<WHOLE>(p.cols, c), 1.0f, w[v]);
+    }
+    for (uint64_t base = (uint64_t)blockIdx.x * kRows; base < p.rows; base += (uint64_t)gridDim.x * kRows) {
+        const uint64_t row = base + r0;
+        const bool in = row < p.rows;
+        const float mean = in ? p.mean[row] : 0.0f, rstd = in ? p.rstd[row] : 0.0f;
+        float h[V][8], dy[V][8], s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t c = first + 8 * (v * THREADS + t), left = in ? left_of<WHOLE>(p.cols, c) : 0;
+            load_chunk<WHOLE>(p.x, kType, row * p.x_stride + c, left, h[v]);
+            load_chunk<WHOLE>(p.dy, kType, row * p.dy_stride + c, left, dy[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t left = left_of<WHOLE>(p.cols, first + 8 * (v * THREADS + t));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                h[v][q] = q < (int)left ? (h[v][q] - mean) * rstd : 0.0f;
+                const float g = dy[v][q] * w[v][q];
+                s[0] += g;
+                s[1] += g * h[v][q];
+                dw[v][q] += dy[v][q] * h[v][q];
+                db[v][q] += dy[v][q];
+            }
+        }
+        if (!p.dx) continue;
+        for (uint32_t other = 0; other < gridDim.y; ++other) {      // the row's other slices
+            if (other == blockIdx.y) continue;
+            for (int v = 0; v < V; ++v) {
+                const uint32_t c = other * kSlice + 8 * (v * THREADS + t), left = in ? left_of<WHOLE>(p.cols, c) : 0;
+                float ox[8], od[8], ow[8];
+                load_chunk<WHOLE>(p.x, kType, row * p.x_stride + c, left, ox);
+                load_chunk<WHOLE>(p.dy, kType, row * p.dy_stride + c, left, od);
+                load_param<WHOLE>(p.weight, p.w_dtype, c, left, 1.0f, ow);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float g = q < (int)left ? od[q] * ow[q] : 0.0f;
+                    s[0] += g;
+                    s[1] += q < (int)left ? g * ((ox[q] - mean) * rstd) : 0.0f;
+                }
+            }
+        }
+        row_sum<THREADS>(s, sh);
+        const float mt = s[0] / cols, mth = s[1] / cols;
+        if (!in) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t c = first + 8 * (v * THREADS + t), left = left_of<WHOLE>(p.cols, c);
+            if (!left) break;
+            float o[8], res[8] = {};
+            if (p.dres) load_chunk<WHOLE>(p.dres, kType, row * p.dres_stride + c, left, res);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = rstd * (dy[v][q] * w[v][q] - mt - h[v][q] * mth) + res[q];
+            store8(p.dx, kType, row * p.dx_stride + c, left, o);
+        }
+    }
+    if (!p.partial) return;
+    if constexpr (kRows > 1) {
+        // the rows' threads add their sums in turn: the first's, plus the second's, ...
+        for (uint32_t r = 0; r < (uint32_t)kRows; ++r) {
+            if (r0 == r) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint32_t at = (v * 8 + q) * THREADS + t;
+                        if (r) {
+                            dw[v][q] += join[at];
+                            db[v][q] += join[kSlice + at];
+                        }
+                        if (r + 1 < (uint32_t)kRows) {
+                            join[at] = dw[v][q];
+                            join[kSlice + at] = db[v][q];
+                        }
+                    }
+            }
+            __syncthreads();
+        }
+        if (r0 != kRows - 1) return;
+    }
+    float *o = p.partial + (uint64_t)blockIdx.x * 2 * p.cols;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const uint32_t c = first + 8 * (v * THREADS + t), left = left_of<WHOLE>(p.cols, c);
+        if (!left) break;
+        store8(o, EC_FP32, c, left, dw[v]);
+        store8(o + p.cols, EC_FP32, c, left, db[v]);
+    }
+}
+
+// Adds the parts in a fixed order: 16 columns by 16 threads that take every
+// 16th part each.
 __global__ __launch_bounds__(256) void norm_grad_sum_kernel(NormGradArgs p) {
-    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= p.cols) return;
-    float dw = 0.0f, db = 0.0f;
-    for (uint32_t q = 0; q < p.parts; ++q) {
-        dw += p.partial[((uint64_t)q * 2) * p.cols + c];
-        db += p.partial[((uint64_t)q * 2 + 1) * p.cols + c];
+    __shared__ float sh[16][17];
+    const uint32_t x = threadIdx.x & 15, y = threadIdx.x >> 4;
+    const uint64_t c = (uint64_t)blockIdx.x * 16 + x, n = 2 * (uint64_t)p.cols;
+    float s = 0.0f;
+    if (c < n)
+        for (uint32_t q = y; q < p.parts; q += 16) s += p.partial[q * n + c];
+    sh[y][x] = s;
+    __syncthreads();
+    if (y || c >= n) return;
+    for (int k = 1; k < 16; ++k) s += sh[k][x];
+    if (c < p.cols) {
+        if (p.dweight) p.dweight[c] = s;
+    } else if (p.dbias) {
+        p.dbias[c - p.cols] = s;
     }
-    if (p.dweight) p.dweight[c] = dw;
-    if (p.dbias) p.dbias[c] = db;
+}
+
+template <bool F32, int BLOCK, int THREADS, int V>
+void run_norm(const NormArgs &a, hipStream_t s) {
+    constexpr int kRows = BLOCK / THREADS;
+    const uint64_t need = (a.rows + kRows - 1) / kRows;
+    const uint32_t blocks = (uint32_t)(need < 65536 ? need : 65536);
+    if (a.cols % 8 == 0)
+        norm_kernel<F32, true, BLOCK, THREADS, V><<<blocks, BLOCK, 0, s>>>(a);
+    else
+        norm_kernel<F32, false, BLOCK, THREADS, V><<<blocks, BLOCK, 0, s>>>(a);
+}
+
+// Threads a row: one wave while a row fits its registers in four chunks a
+// lane and there are rows enough for every CU (no barrier in the sums), more
+// for longer rows, and for few rows, where the time is that of one row.
+template <bool F32>
+void pick_norm(const NormArgs &a, hipStream_t s) {
+    const uint32_t c = a.cols;
+    if (c <= 512)
+        run_norm<F32, 256, 64, 1>(a, s);
+    else if (c <= 2048 && a.rows >= 1024)
+        c <= 1024 ? run_norm<F32, 256, 64, 2>(a, s) : run_norm<F32, 256, 64, 4>(a, s);
+    else if (c <= 8192)
+        c <= 2048 ? run_norm<F32, 256, 256, 1>(a, s)
+                  : c <= 4096 ? run_norm<F32, 256, 256, 2>(a, s) : run_norm<F32, 256, 256, 4>(a, s);
+    else if (c <= 16384)
+        run_norm<F32, 1024, 1024, 2>(a, s);
+    else
+        c <= 32768 ? run_norm<F32, 1024, 1024, 4>(a, s) : run_norm<F32, 1024, 1024, 8>(a, s);
+}
+
+template <bool F32, int THREADS, int V>
+void run_norm_grad(const NormGradArgs &a, hipStream_t s) {
+    const dim3 grid(a.parts, (a.cols + THREADS * V * 8 - 1) / (THREADS * V * 8));
+    if (a.cols % 8 == 0)
+        norm_grad_kernel<F32, true, THREADS, V><<<grid, 512, 0, s>>>(a);
+    else
+        norm_grad_kernel<F32, false, THREADS, V><<<grid, 512, 0, s>>>(a);
+}
+
+// Threads a row in the backward pass: two chunks a thread, whose sums and
+// values leave room for four waves a SIMD.
+uint32_t grad_threads(uint64_t cols) { return cols <= 512 ? 64 : cols <= 2048 ? 128 : cols <= 4096 ? 256 : 512; }
+
+template <bool F32>
+void pick_norm_grad(const NormGradArgs &a, hipStream_t s) {
+    switch (grad_threads(a.cols)) {
+        case 64: run_norm_grad<F32, 64, 1>(a, s); break;
+        case 128: a.cols <= 1024 ? run_norm_grad<F32, 128, 1>(a, s) : run_norm_grad<F32, 128, 2>(a, s); break;
+        case 256: run_norm_grad<F32, 256, 2>(a, s); break;
+        default: run_norm_grad<F32, 512, 2>(a, s);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
     if (!a.rows) return hipSuccess;
-    if (a.dtype == EC_FP32)
-        norm_kernel<true><<<(uint32_t)a.rows, 256, 0, s>>>(a);
-    else
-        norm_kernel<false><<<(uint32_t)a.rows, 256, 0, s>>>(a);
+    a.dtype == EC_FP32 ? pick_norm<true>(a, s) : pick_norm<false>(a, s);
     return hipGetLastError();
 }
 
-uint32_t norm_grad_parts(uint64_t rows, uint64_t) { return rows ? (uint32_t)((rows + 127) / 128 < 256 ? (rows + 127) / 128 : 256) : 1; }
+// Workgroups of the backward pass, each with a row of sums to add: two a CU.
+uint32_t norm_grad_parts(uint64_t rows, uint64_t cols) {
+    const uint64_t at_once = 512 / grad_threads(cols), need = (rows + at_once - 1) / at_once;
+    return (uint32_t)(need < 1 ? 1 : need < 512 ? need : 512);
+}
 
 hipError_t launch_norm_grad(const NormGradArgs &a, hipStream_t s) {
-    const dim3 cols((a.cols + 255) / 256);
-    if (a.rows && a.dx) {
-        if (a.dtype == EC_FP32)
-            norm_grad_kernel<true><<<(uint32_t)a.rows, 256, 0, s>>>(a);
-        else
-            norm_grad_kernel<false><<<(uint32_t)a.rows, 256, 0, s>>>(a);
-    }
-    if (a.dweight || a.dbias) {
-        if (a.dtype == EC_FP32)
-            norm_grad_weight_kernel<true><<<dim3(cols.x, a.parts), 256, 0, s>>>(a);
-        else
-            norm_grad_weight_kernel<false><<<dim3(cols.x, a.parts), 256, 0, s>>>(a);
-        norm_grad_sum_kernel<<<cols, 256, 0, s>>>(a);
-    }
+    if (a.dx || a.partial) a.dtype == EC_FP32 ? pick_norm_grad<true>(a, s) : pick_norm_grad<false>(a, s);
+    if (a.partial) norm_grad_sum_kernel<<<(2 * a.cols + 15) / 16, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -461,16 +461,60 @@ __global__ __launch_bounds__(256) void copy_rows_kernel(const E *p, uint64_t str
 
 // ---------------------------------------------------------------- column sums
 //
-// db[n] = sum of dy's rows; one thread per column, rows of the group in order.
-__global__ __launch_bounds__(256) void column_sum_kernel(ColumnSumArgs p) {
+// db[n] = sum of dy's rows.  A workgroup takes 128 columns of one part of a
+// group's rows, 16 threads of eight columns by 16 rows; where that alone does
+// not fill the card the rows are cut into parts, added in their order after.
+constexpr uint32_t kSumCols = 128;
+
+__global__ __launch_bounds__(256) void column_sum_kernel(ColumnSumArgs p, float *out, uint32_t parts) {
+    __shared__ float sh[16][kSumCols + 4];
+    const uint32_t g = blockIdx.y, part = blockIdx.z;
     uint32_t lo = 0, hi = p.m;
-    const uint32_t g = blockIdx.y;
-    if (p.groups) group_range(p.offsets, p.m, g, &lo, &hi);
-    const uint32_t n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= p.n) return;
+    if (p.groups) {
+        if (blockIdx.x == 0 && g == 0 && part == 0 && threadIdx.x < 64) check_offsets(p.offsets, p.groups, p.m, p.status);
+        group_range(p.offsets, p.m, g, &lo, &hi);
+    }
+    const uint64_t len = hi - lo;
+    hi = lo + (uint32_t)(len * (part + 1) / parts);
+    lo += (uint32_t)(len * part / parts);
+    const uint32_t x = (threadIdx.x & 15) * 8, y = threadIdx.x >> 4, n = blockIdx.x * kSumCols + x;
+    const uint32_t left = p.n > n ? p.n - n : 0;
+    float s[8] = {};
+    if (left) {
+        uint32_t i = lo + y;
+        for (; i + 48 < hi; i += 64) {      // four rows on the way at a time
+            float v[4][8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) load8_bf16(p.dy, (uint64_t)(i + 16 * k) * p.dy_stride + n, left, v[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) s[q] += v[k][q];
+        }
+        for (; i < hi; i += 16) {
+            float v[8];
+            load8_bf16(p.dy, (uint64_t)i * p.dy_stride + n, left, v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s[q] += v[q];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sh[y][x + q] = s[q];
+    __syncthreads();
+    const uint32_t c = blockIdx.x * kSumCols + threadIdx.x;
+    if (threadIdx.x >= kSumCols || c >= p.n) return;
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t += sh[k][threadIdx.x];
+    out[((uint64_t)part * gridDim.y + g) * p.n + c] = t;
+}
+
+__global__ __launch_bounds__(256) void column_join_kernel(const float *in, float *db, uint64_t n, uint32_t parts) {
+    const uint64_t c = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= n) return;
     float s = 0.0f;
-    for (uint32_t i = lo; i < hi; ++i) s += bf16_to_f32(p.dy[i * p.dy_stride + n]);
-    p.db[(uint64_t)g * p.n + n] = s;
+    for (uint32_t q = 0; q < parts; ++q) s += in[q * n + c];
+    db[c] = s;
 }
 
 // ---------------------------------------------------------------------- plan
@@ -622,9 +666,25 @@ hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_column_sum(const ColumnSumArgs &a, hipStream_t s) {
+static uint32_t column_parts(const ColumnSumArgs &a) {
+    const uint64_t groups = a.groups ? a.groups : 1, blocks = ceil_div(a.n, kSumCols) * groups;
+    uint64_t parts = ceil_div(512, blocks), most = ceil_div(a.m, groups * 64);
+    if (parts > most) parts = most;
+    return (uint32_t)(parts < 1 ? 1 : parts > 64 ? 64 : parts);
+}
+
+uint64_t column_sum_workspace(const ColumnSumArgs &a) {
+    const uint32_t parts = a.n ? column_parts(a) : 1;
+    return parts > 1 ? (uint64_t)parts * (a.groups ? a.groups : 1) * a.n * 4 : 0;
+}
+
+hipError_t launch_column_sum(const ColumnSumArgs &a, float *workspace, hipStream_t s) {
     if (!a.n) return hipSuccess;
-    column_sum_kernel<<<dim3((a.n + 255) / 256, a.groups ? a.groups : 1), 256, 0, s>>>(a);
+    const uint32_t parts = column_parts(a), groups = a.groups ? a.groups : 1;
+    const uint64_t n = (uint64_t)groups * a.n;
+    column_sum_kernel<<<dim3((uint32_t)ceil_div(a.n, kSumCols), groups, parts), 256, 0, s>>>(a, parts > 1 ? workspace : a.db,
+                                                                                           parts);
+    if (parts > 1) column_join_kernel<<<(uint32_t)ceil_div(n, 256), 256, 0, s>>>(workspace, a.db, n, parts);
     return hipGetLastError();
 }
 
