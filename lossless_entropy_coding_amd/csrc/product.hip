@@ -9,18 +9,29 @@ namespace {
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 
 // ------------------------------------------------------------- tiled product
 //
-// A workgroup of four waves makes a TI x TJ tile of D, WI x WJ waves side by
-// side, each a block of 32 x 32 tiles of the matrix units.  The contraction
-// is walked in stages of 64 bytes (32 bf16 or 64 e4m3 values); S stages of
-// both factors lie in LDS and are filled by loads that bypass the registers.
-// The fragments of a stage are read while the products of the one before run.
+// A workgroup of WI x WJ waves makes a TI x TJ tile of D, each wave a block
+// of 32 x 32 tiles of the matrix units.  The contraction is walked in stages
+// of 64 bytes (32 bf16 or 64 e4m3 values); S stages of both factors lie in
+// LDS and are filled by loads that bypass the registers.  The fragments of a
+// stage are read while the products of the one before run.
+//
+// What bounds it: every value of a tile's rows passes the CU's load path, 64
+// bytes a clock, once a tile, so large tiles halve that (256 x 256: half of
+// the matrix units' time at their full rate, 128 x 128: all of it), and the
+// power limit, which brings the clock under full load from 2.4 to 1.6 - 2.0
+// GHz (the same product of zeros runs 1.25 times as fast).  Eight waves of
+// 128 x 64 keep two waves a SIMD; four of 128 x 128 need all registers and
+// spill.  Asking for lines ahead of their stage, or loading two stages at a
+// time (whole 128-byte lines), was slower where the weights come from HBM.
 template <int TI_, int TJ_, int WI_, int WJ_, int S_, int PER_CU_>
 struct Shape {
-    static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, S = S_, PER_CU = PER_CU_;
-    static constexpr int NI = TI / WI / 32, NJ = TJ / WJ / 32;
+    static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, S = S_;
+    static constexpr int PER_CU = PER_CU_;              // workgroups whose LDS fits a CU
+    static constexpr int NI = TI / WI / 32, NJ = TJ / WJ / 32, W = WI * WJ, THREADS = 64 * W;
     static constexpr int kStage = (TI + TJ) * 64;
 };
 
@@ -34,21 +45,23 @@ __device__ __forceinline__ constexpr uint32_t unit_order(uint32_t c, uint32_t T)
 // One factor's tile of T rows (i or j) by one stage.
 //
 // Rows contiguous along the contraction: the tile holds row r at r * 64, its
-// four 16-byte chunks in the order chunk ^ (r / 2 % 4), so that eight rows'
-// equal chunks cover all banks.  Contraction outermost (OUTER): the tile
+// four 16-byte chunks in the order chunk ^ (r / 4 % 4), so that 16 rows' equal
+// chunks cover all 64 banks.  Contraction outermost (OUTER): the tile
 // holds stage row c at c * 2 T, its 32-byte units in the order unit ^ h(c),
 // h = 2 (c % 4) + c / 2 % 2 (modulo the units of a row), so that the four rows of a transposed read fall
 // into different banks.  A load writes 1 KB of consecutive LDS per wave; the
 // order is made by which address each lane reads.
-template <int T, bool OUTER, int ES>
+template <int T, bool OUTER, int ES, int W>
 struct Factor {
-    static constexpr int kBytes = T * kStageBytes, kInstr = kBytes / 1024, kLoads = (kInstr + 3) / 4;
+    static constexpr int kBytes = T * kStageBytes, kInstr = kBytes / 1024, kLoads = (kInstr + W - 1) / W;
     static constexpr int kDepth = kStageBytes / ES;     // contraction values a stage
     static constexpr int kRowsPer = 1024 / (T * 2);     // OUTER: stage rows a load
     uint32_t off[kLoads];                               // per lane
     uint64_t base;                                      // of the stage
     int64_t left;                                       // bytes from base to the end of what may be read
     uint64_t step;
+    i32x4 d;                                            // the buffer of the stage being loaded
+    uint32_t out;                                       // kOutside on the lanes past the contraction's end
 
     // rows: of the tile that exist; stride in elements; first and count along the contraction
     __device__ __forceinline__ void init(const void *p, uint64_t stride, uint64_t row0, uint32_t rows, uint32_t c0,
@@ -56,7 +69,7 @@ struct Factor {
         const uint64_t sb = stride * ES;
 #pragma unroll
         for (int n = 0; n < kLoads; ++n) {
-            const uint32_t q = (n * 4 + wave) % kInstr;
+            const uint32_t q = (n * W + wave) % kInstr;
             if constexpr (OUTER) {
                 constexpr uint32_t kLane = 64 / kRowsPer;
                 const uint32_t c = q * kRowsPer + lane / kLane, pos = lane % kLane;
@@ -64,7 +77,7 @@ struct Factor {
                 off[n] = c * (uint32_t)sb + ((((pos >> 1) ^ h) << 1) | (pos & 1)) * 16;
             } else {
                 const uint32_t r = q * 16 + (lane >> 2);
-                off[n] = r * (uint32_t)sb + ((lane & 3) ^ ((r >> 1) & 3)) * 16;
+                off[n] = r * (uint32_t)sb + ((lane & 3) ^ ((r >> 2) & 3)) * 16;
             }
         }
         if constexpr (OUTER) {
@@ -79,26 +92,26 @@ struct Factor {
         left = (left + 3) & ~3ll;           // whole dwords: the last one holds valid elements
     }
 
-    // Loads the next stage into LDS at `at`; `rest` is what remains of the
+    // Makes the next stage the one to load; `rest` is what remains of the
     // contraction, in bytes of a row (not OUTER): chunks past it read as zero.
-    __device__ __forceinline__ void load(uint32_t at, int32_t rest, uint32_t wave, uint32_t lane) {
-        i32x4 d;
+    __device__ __forceinline__ void next(int32_t rest, uint32_t lane) {
         const int64_t n = left < 0 ? 0 : left > 0x7FFFFFFF ? 0x7FFFFFFF : left;
         d[0] = __builtin_amdgcn_readfirstlane((int)base);
         d[1] = __builtin_amdgcn_readfirstlane((int)(base >> 32) & 0xFFFF);
         d[2] = __builtin_amdgcn_readfirstlane(rest > 0 ? (int)n : 0);
         d[3] = 0x00027000;
-        uint32_t out = 0;
-        if constexpr (!OUTER) out = (int32_t)(((lane & 3) ^ ((lane >> 3) & 3)) * 16) < rest ? 0 : kOutside;
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-            const uint32_t q = (k * 4 + wave) % kInstr;
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at + q * 1024),
-                         "v"(off[k] | out), "s"(d)
-                         : "memory");
-        }
+        out = 0;
+        if constexpr (!OUTER) out = (int32_t)(((lane & 3) ^ ((lane >> 4) & 3)) * 16) < rest ? 0 : kOutside;
         base += step;
         left -= (int64_t)step;
+    }
+
+    // Load k of that stage, to the stage's place in LDS.
+    __device__ __forceinline__ void load(int k, uint32_t at, uint32_t wave) {
+        const uint32_t q = (k * W + wave) % kInstr;
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at + q * 1024),
+                     "v"(off[k] | out), "s"(d)
+                     : "memory", "m0");
     }
 };
 
@@ -112,131 +125,152 @@ struct Fragments {
             const uint32_t unit = wave_row / 16 + t * 2 + ((lane >> 4) & 1);
             return c * (2 * T) + (unit ^ h) * 32 + (lane & 3) * 8;
         } else {
-            return (wave_row + t * 32 + (lane & 31)) * 64 + ((lane >> 5) ^ ((lane >> 1) & 3)) * 16;
+            return (wave_row + t * 32 + (lane & 31)) * 64 + ((lane >> 5) ^ ((lane >> 2) & 3)) * 16;
         }
     }
 
-    static __device__ __forceinline__ void read(u32x4 (&f)[N][2], lds_char *stage, const uint32_t *offs) {
-#pragma unroll
-        for (int t = 0; t < N; ++t) {
-            if constexpr (OUTER) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    union {
-                        s16x4 h[2];
-                        u32x4 w;
-                    } u;
-                    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + offs[t] + s * 16 * 2 * T));
-                    u.h[1] =
-                        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + offs[t] + (s * 16 + 4) * 2 * T));
-                    f[t][s] = u.w;
-                }
-            } else {
-                f[t][0] = *(lds_u32x4 *)(stage + offs[0] + t * 2048);
-                f[t][1] = *(lds_u32x4 *)(stage + (offs[0] ^ 32) + t * 2048);
-            }
+    // Half s of tile t.
+    static __device__ __forceinline__ void read(u32x4 (&f)[N][2], lds_char *stage, const uint32_t *offs, int t, int s) {
+        if constexpr (OUTER) {
+            union {
+                s16x4 h[2];
+                u32x4 w;
+            } u;
+            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + offs[t] + s * 16 * 2 * T));
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + offs[t] + (s * 16 + 4) * 2 * T));
+            f[t][s] = u.w;
+        } else {
+            f[t][s] = *(lds_u32x4 *)(stage + (offs[0] ^ (s * 32)) + t * 2048);
         }
     }
 };
 
+// A stage's products, in the order of the fragments' halves; between(g) is
+// called before each of kGroups groups of them, for what goes on beside them.
 template <int NI, int NJ, bool E4M3>
-__device__ __forceinline__ void multiply(f32x16 (&acc)[NI][NJ], const u32x4 (&a)[NI][2], const u32x4 (&b)[NJ][2]) {
-    if constexpr (E4M3) {
-        // e4m3 values are exact in bf16, and the products of bf16 are added in
-        // 32 bits.  The e4m3 instructions are not used: they cut the products
-        // they add to a few bits below the largest (measured: sums of 16 off
-        // by up to 2^-14 of the sum of magnitudes, against 2^-26 here), where
-        // sums are to be held in 32 bits.
+struct Multiply {
+    static constexpr int kGroups = E4M3 ? 4 : 2 * NI;
+
+    template <class F>
+    static __device__ __forceinline__ void run(f32x16 (&acc)[NI][NJ], const u32x4 (&a)[NI][2], const u32x4 (&b)[NJ][2],
+                                               F between) {
+        if constexpr (E4M3) {
+            // e4m3 values are exact in bf16, and the products of bf16 are added in
+            // 32 bits.  The e4m3 instructions are not used: they cut the products
+            // they add to a few bits below the largest (measured: sums of 16 off
+            // by up to 2^-14 of the sum of magnitudes, against 2^-26 here), where
+            // sums are to be held in 32 bits.
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            bf16x8 fa[NI], fb[NJ];
+            for (int s = 0; s < 4; ++s) {
+                between(s);
+                bf16x8 fa[NI], fb[NJ];
 #pragma unroll
-            for (int x = 0; x < NI; ++x) fa[x] = e4m3_to_bf16x8(a[x][s >> 1][2 * (s & 1)], a[x][s >> 1][2 * (s & 1) + 1]);
-#pragma unroll
-            for (int y = 0; y < NJ; ++y) fb[y] = e4m3_to_bf16x8(b[y][s >> 1][2 * (s & 1)], b[y][s >> 1][2 * (s & 1) + 1]);
-#pragma unroll
-            for (int x = 0; x < NI; ++x)
+                for (int x = 0; x < NI; ++x)
+                    fa[x] = e4m3_to_bf16x8(a[x][s >> 1][2 * (s & 1)], a[x][s >> 1][2 * (s & 1) + 1]);
 #pragma unroll
                 for (int y = 0; y < NJ; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[y], fa[x], acc[x][y], 0, 0, 0);
+                    fb[y] = e4m3_to_bf16x8(b[y][s >> 1][2 * (s & 1)], b[y][s >> 1][2 * (s & 1) + 1]);
+#pragma unroll
+                for (int x = 0; x < NI; ++x)
+#pragma unroll
+                    for (int y = 0; y < NJ; ++y)
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[y], fa[x], acc[x][y], 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int x = 0; x < NI; ++x) {
+                    between(s * NI + x);
+#pragma unroll
+                    for (int y = 0; y < NJ; ++y)
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b[y][s]),
+                                                                            __builtin_bit_cast(bf16x8, a[x][s]),
+                                                                            acc[x][y], 0, 0, 0);
+                }
         }
-    } else {
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int x = 0; x < NI; ++x)
-#pragma unroll
-                for (int y = 0; y < NJ; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b[y][s]),
-                                                                        __builtin_bit_cast(bf16x8, a[x][s]), acc[x][y],
-                                                                        0, 0, 0);
     }
-}
+};
 
 // ----------------------------------------------------------------- epilogue
 
 // The wave's accumulators hold, of each 32 x 32 tile, row i = lane % 32 and
-// columns 8 g + 4 (lane / 32) + r in register 4 g + r.  Two halves of the
-// wave exchange registers so that a lane has eight consecutive columns.
-__device__ __forceinline__ void eight_columns(const f32x16 &c, int q, float *v) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[8 * q + r]), __float_as_uint(c[8 * q + 4 + r]),
-                                                        false, false);
-        v[r] = __uint_as_float(s[0]);
-        v[4 + r] = __uint_as_float(s[1]);
+// columns 8 g + 4 (lane / 32) + r in register 4 g + r.  32 rows at a time go
+// through the wave's part of LDS (fp32, 16-byte chunks in the order chunk ^
+// row), so that a lane has eight consecutive columns, the same ones in every
+// row, and the lanes of a row side by side read and write whole lines.
+template <int NJ>
+struct Turn {
+    static constexpr int kLanes = NJ * 4, kRows = 64 / kLanes, kBytes = 32 * NJ * 128;  // lanes a row, rows at a time
+
+    static __device__ __forceinline__ uint32_t chunk_at(uint32_t row, uint32_t chunk) {
+        return row * (NJ * 128) + (chunk ^ (NJ == 1 ? row >> 1 & 7 : row & (NJ * 8 - 1))) * 16;
     }
-}
+
+    static __device__ __forceinline__ void put(lds_char *mem, const f32x16 (&acc)[NJ], uint32_t lane) {
+#pragma unroll
+        for (int y = 0; y < NJ; ++y)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *(lds_f32x4 *)(mem + chunk_at(lane & 31, y * 8 + g * 2 + (lane >> 5))) =
+                    f32x4{acc[y][4 * g], acc[y][4 * g + 1], acc[y][4 * g + 2], acc[y][4 * g + 3]};
+    }
+
+    static __device__ __forceinline__ void get(lds_char *mem, uint32_t row, uint32_t lane, float *v) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 w = *(lds_f32x4 *)(mem + chunk_at(row, lane % kLanes * 2 + h));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * h + r] = w[r];
+        }
+    }
+};
 
 template <int NI, int NJ, int OP, int ACT>
 __device__ __forceinline__ void finish_tiles(const ProductArgs &p, f32x16 (&acc)[NI][NJ], uint32_t g, uint32_t i0,
-                                             uint32_t i1, uint32_t j0, bool zero) {
-    const uint32_t lane = threadIdx.x & 63;
-    float xs[NI];
+                                             uint32_t i1, uint32_t j0, bool zero, lds_char *mem) {
+    using R = Turn<NJ>;
+    constexpr int kSteps = 32 / R::kRows, kAtOnce = kSteps < 4 ? kSteps : 4;
+    const uint32_t lane = threadIdx.x & 63, j = j0 + lane % R::kLanes * 8;
     const float os = OP == EC_LINEAR_FORWARD && p.out_scale ? *p.out_scale : 1.0f;
+    const Columns c = load_columns<OP>(p, g, j);
 #pragma unroll
     for (int x = 0; x < NI; ++x) {
-        const uint32_t i = i0 + x * 32 + (lane & 31);
-        xs[x] = 1.0f;
-        if (OP == EC_LINEAR_FORWARD && p.x_scale && i < i1) xs[x] = p.x_scale[p.x_scales > 1 ? i : 0];
-    }
+        R::put(mem, acc[x], lane);
 #pragma unroll
-    for (int y = 0; y < NJ; ++y) {
-        Columns c[2];
-        float side[NI][2][8];
+        for (int t0 = 0; t0 < kSteps; t0 += kAtOnce) {
+            float side[kAtOnce][8], xs[kAtOnce];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint32_t j = j0 + y * 32 + q * 16 + (lane >> 5) * 8;
-            c[q] = load_columns<OP>(p, g, j);
+            for (int t = 0; t < kAtOnce; ++t) {
+                const uint32_t i = i0 + x * 32 + (t0 + t) * R::kRows + lane / R::kLanes;
+                xs[t] = 1.0f;
+                if (i < i1) {
+                    if (OP == EC_LINEAR_FORWARD && p.x_scale) xs[t] = p.x_scale[p.x_scales > 1 ? i : 0];
+                    load_side<OP>(p, i, j, c.left, side[t]);
+                }
+            }
 #pragma unroll
-            for (int x = 0; x < NI; ++x) {
-                const uint32_t i = i0 + x * 32 + (lane & 31);
-                if (i < i1) load_side<OP>(p, i, j, c[q].left, side[x][q]);
+            for (int t = 0; t < kAtOnce; ++t) {
+                const uint32_t row = (t0 + t) * R::kRows + lane / R::kLanes, i = i0 + x * 32 + row;
+                float v[8];
+                R::get(mem, row, lane, v);
+                if (i < i1) finish8<OP, ACT>(p, g, i, j, v, c, side[t], xs[t], os, zero);
             }
         }
-#pragma unroll
-        for (int x = 0; x < NI; ++x)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint32_t i = i0 + x * 32 + (lane & 31), j = j0 + y * 32 + q * 16 + (lane >> 5) * 8;
-                float v[8];
-                eight_columns(acc[x][y], q, v);
-                if (i < i1) finish8<OP, ACT>(p, g, i, j, v, c[q], side[x][q], xs[x], os, zero);
-            }
     }
 }
 
 template <int NI, int NJ, int OP>
 __device__ __forceinline__ void finish(const ProductArgs &p, f32x16 (&acc)[NI][NJ], uint32_t g, uint32_t i0,
-                                       uint32_t i1, uint32_t j0, bool zero) {
+                                       uint32_t i1, uint32_t j0, bool zero, lds_char *mem) {
     if constexpr (OP == EC_LINEAR_GRAD_WEIGHT) {
-        finish_tiles<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero);
+        finish_tiles<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero, mem);
     } else {
         switch (p.act) {
-            case EC_ACT_GELU: finish_tiles<NI, NJ, OP, EC_ACT_GELU>(p, acc, g, i0, i1, j0, zero); break;
-            case EC_ACT_SILU: finish_tiles<NI, NJ, OP, EC_ACT_SILU>(p, acc, g, i0, i1, j0, zero); break;
-            case EC_ACT_RELU: finish_tiles<NI, NJ, OP, EC_ACT_RELU>(p, acc, g, i0, i1, j0, zero); break;
-            default: finish_tiles<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero);
+            case EC_ACT_GELU: finish_tiles<NI, NJ, OP, EC_ACT_GELU>(p, acc, g, i0, i1, j0, zero, mem); break;
+            case EC_ACT_SILU: finish_tiles<NI, NJ, OP, EC_ACT_SILU>(p, acc, g, i0, i1, j0, zero, mem); break;
+            case EC_ACT_RELU: finish_tiles<NI, NJ, OP, EC_ACT_RELU>(p, acc, g, i0, i1, j0, zero, mem); break;
+            default: finish_tiles<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero, mem);
         }
     }
 }
@@ -304,12 +338,12 @@ __device__ __forceinline__ Place find_place(const ProductArgs &p, uint32_t block
 }
 
 template <class T, int OP, bool E4M3>
-__global__ __launch_bounds__(256, T::PER_CU) void product_kernel(ProductArgs p) {
+__global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
     constexpr bool kOuterA = OP == EC_LINEAR_GRAD_WEIGHT, kOuterB = OP != EC_LINEAR_FORWARD;
     constexpr int kES = E4M3 ? 1 : 2, kDepth = kStageBytes / kES;
     constexpr int NI = T::NI, NJ = T::NJ, S = T::S;
-    using FA = Factor<T::TI, kOuterA, kES>;
-    using FB = Factor<T::TJ, kOuterB, kES>;
+    using FA = Factor<T::TI, kOuterA, kES, T::W>;
+    using FB = Factor<T::TJ, kOuterB, kES, T::W>;
     using RA = Fragments<T::TI, NI, kOuterA>;
     using RB = Fragments<T::TJ, NJ, kOuterB>;
     __shared__ __attribute__((aligned(1024))) char lds[S * T::kStage];
@@ -354,34 +388,59 @@ __global__ __launch_bounds__(256, T::PER_CU) void product_kernel(ProductArgs p) 
 #pragma unroll
         for (int y = 0; y < NJ; ++y) bo[y] = T::TI * kStageBytes + RB::at(wj, y, lane);
 
-        const auto fill = [&](uint32_t stage) {
-            const uint32_t at = mem_at + stage * T::kStage;
-            fa.load(at, rest, wave, lane);
-            fb.load(at + FA::kBytes, rest, wave, lane);
-            rest -= kStageBytes;
-        };
-        constexpr int kLoads = FA::kLoads + FB::kLoads;
-        u32x4 af[2][NI][2], bf[2][NJ][2];
+        constexpr int kLoads = FA::kLoads + FB::kLoads, kReads = 2 * (NI + NJ);
         uint32_t fill_at = 0, read_at = 0;
+        const auto load = [&](int k) {      // of kLoads
+            if (k == 0) fa.next(rest, lane);
+            if (k == FA::kLoads) fb.next(rest, lane);
+            const uint32_t at = mem_at + fill_at * T::kStage;
+            if (k < FA::kLoads)
+                fa.load(k, at, wave);
+            else
+                fb.load(k - FA::kLoads, at + FA::kBytes, wave);
+            if (k == kLoads - 1) {
+                fill_at = fill_at + 1 == S ? 0 : fill_at + 1;
+                rest -= kStageBytes;
+            }
+        };
+        u32x4 af[2][NI][2], bf[2][NJ][2];
+        const auto read = [&](int r, int to, uint32_t stage) {      // in the order of their use
+            const int s = r / (NI + NJ), t = r % (NI + NJ);
+            if (t < NJ)
+                RB::read(bf[to], mem + stage * T::kStage, bo, t, s);
+            else
+                RA::read(af[to], mem + stage * T::kStage, ao, t - NJ, s);
+        };
 #pragma unroll
-        for (int s = 0; s < S; ++s) fill(s);
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) load(k);
         // stage 0 has arrived, everywhere
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * kLoads) : "memory");
         __builtin_amdgcn_s_barrier();
-        RA::read(af[0], mem, ao);
-        RB::read(bf[0], mem, bo);
-        // Stage k: its fragments are in registers (or on the way); once every
+#pragma unroll
+        for (int r = 0; r < kReads; ++r) read(r, 0, 0);
+        // Stage k: its fragments are in registers (or on the way).  Once every
         // wave has them, its LDS takes stage k + S, and stage k + 1 is read.
+        // The loads are spread over the products of stage k (a wave whose load
+        // finds the queue full issues no products either), the reads over
+        // their first half, so that the wait for the last one is short.
         const auto step = [&](int now) {
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * kLoads) : "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            fill(fill_at);
-            fill_at = fill_at + 1 == S ? 0 : fill_at + 1;
             read_at = read_at + 1 == S ? 0 : read_at + 1;
-            RA::read(af[1 - now], mem + read_at * T::kStage, ao);
-            RB::read(bf[1 - now], mem + read_at * T::kStage, bo);
-            multiply<NI, NJ, E4M3>(acc, af[now], bf[now]);
+            using M = Multiply<NI, NJ, E4M3>;
+            M::run(acc, af[now], bf[now], [&](int g) {
+                constexpr int G = M::kGroups;
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int r = 0; r < kReads; ++r)
+                    if (r >= 2 * g * kReads / G && r < 2 * (g + 1) * kReads / G) read(r, 1 - now, read_at);
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k)
+                    if (k >= g * kLoads / G && k < (g + 1) * kLoads / G) load(k);
+            });
         };
         for (uint32_t k = 0;;) {
             step(0);
@@ -407,14 +466,17 @@ __global__ __launch_bounds__(256, T::PER_CU) void product_kernel(ProductArgs p) 
                 }
         return;
     }
-    finish<NI, NJ, OP>(p, acc, q.group, q.i0 + wi, q.i1, q.j0 + wj, q.zero);
+    __syncthreads();                        // every wave has read its last stage
+    static_assert(T::W * Turn<NJ>::kBytes <= S * T::kStage, "the turned tiles fit the stages' LDS");
+    finish<NI, NJ, OP>(p, acc, q.group, q.i0 + wi, q.i1, q.j0 + wj, q.zero, (lds_char *)lds + wave * Turn<NJ>::kBytes);
 }
 
 // Adds the splits' sums in their order and finishes: a workgroup takes one
 // 32 x 32 tile of each of the four waves of a tile.
 template <class T, int OP>
-__global__ __launch_bounds__(256) void join_kernel(ProductArgs p) {
+__global__ __launch_bounds__(T::THREADS) void join_kernel(ProductArgs p) {
     constexpr int NI = T::NI, NJ = T::NJ;
+    __shared__ __attribute__((aligned(1024))) char lds[T::W * Turn<1>::kBytes];
     const uint32_t tile = blockIdx.x / (NI * NJ), xy = blockIdx.x - tile * (NI * NJ), x = xy / NJ, y = xy - x * NJ;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t tiles = (uint64_t)p.tiles_i * p.tiles_j;
@@ -422,6 +484,7 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs p) {
     band_order(tile, p.tiles_i, p.tiles_j, &ti, &tj);
     f32x16 acc[1][1] = {};
     const float *o = p.partial + (uint64_t)tile * (T::TI * T::TJ) + wave * (NI * NJ * 1024) + xy * 1024 + lane * 4;
+#pragma unroll 4                            // loads of four splits on the way
     for (uint32_t s = 0; s < p.splits; ++s, o += tiles * (T::TI * T::TJ))
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -430,7 +493,107 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs p) {
             for (int k = 0; k < 4; ++k) acc[0][0][4 * r + k] += v[k];
         }
     const uint32_t i0 = ti * T::TI, wi = wave / T::WJ * (NI * 32) + x * 32, wj = wave % T::WJ * (NJ * 32) + y * 32;
-    finish<1, 1, OP>(p, acc, 0, i0 + wi, min(p.I, i0 + T::TI), tj * T::TJ + wj, false);
+    finish<1, 1, OP>(p, acc, 0, i0 + wi, min(p.I, i0 + T::TI), tj * T::TJ + wj, false,
+                      (lds_char *)lds + wave * Turn<1>::kBytes);
+}
+
+// ------------------------------------------------------------------ few rows
+//
+// Up to 32 rows (of a group): the time is that of reading B once, so nothing
+// is staged.  A workgroup takes 16 columns and RT x 16 rows, its W waves a
+// part of the contraction each; a lane loads 16 bytes of its column's row of
+// B, and of its rows of A, at a time, 64 bytes of a row in a wave's load, and
+// the waves' sums are joined in LDS in the waves' order.
+template <int RT, int W>
+struct Few {
+    static constexpr int TI = RT * 16, TJ = 16;
+    static constexpr int kAtOnce = 8;                   // loads of B on the way in a lane
+};
+
+template <int RT, bool E4M3>
+__device__ __forceinline__ void few_multiply(f32x4 (&acc)[RT], const u32x4 &b, const u32x4 (&a)[RT]) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        if constexpr (E4M3) {
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_to_bf16x8(b[0], b[1]), e4m3_to_bf16x8(a[t][0], a[t][1]),
+                                                             acc[t], 0, 0, 0);
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_to_bf16x8(b[2], b[3]), e4m3_to_bf16x8(a[t][2], a[t][3]),
+                                                             acc[t], 0, 0, 0);
+        } else {
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a[t]),
+                                                             acc[t], 0, 0, 0);
+        }
+    }
+}
+
+template <int RT, int ACT>
+__device__ __forceinline__ void few_finish(const ProductArgs &p, const Place &q, const float *sums, uint32_t waves) {
+    const uint32_t t = threadIdx.x, i = q.i0 + (t >> 1), j = q.j0 + (t & 1) * 8;
+    if (t >= RT * 32 || i >= q.i1) return;
+    const Columns c = load_columns<EC_LINEAR_FORWARD>(p, q.group, j);
+    float side[8], v[8] = {};
+    load_side<EC_LINEAR_FORWARD>(p, i, j, c.left, side);
+    const float xs = p.x_scale ? p.x_scale[p.x_scales > 1 ? i : 0] : 1.0f, os = p.out_scale ? *p.out_scale : 1.0f;
+    for (uint32_t w = 0; w < waves; ++w)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 s = *(const f32x4 *)(sums + (w * (RT * 16) + (t >> 1)) * 20 + (t & 1) * 8 + h * 4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * h + r] += s[r];
+        }
+    finish8<EC_LINEAR_FORWARD, ACT>(p, q.group, i, j, v, c, side, xs, os, q.zero);
+}
+
+template <int RT, int W, bool E4M3>
+__global__ __launch_bounds__(W * 64) void few_rows_kernel(ProductArgs p) {
+    using T = Few<RT, W>;
+    constexpr int ES = E4M3 ? 1 : 2, U = T::kAtOnce;
+    __shared__ __attribute__((aligned(16))) float sums[W * RT * 16 * 20];   // [wave][row][16 columns and a gap]
+    if (p.groups && blockIdx.x == 0 && threadIdx.x < 64) check_offsets(p.offsets, p.groups, p.I, p.status);
+    const Place q = find_place<T, EC_LINEAR_FORWARD>(p, blockIdx.x);
+    if (q.none) return;
+    const uint32_t lane = threadIdx.x & 63, row = lane & 15, part = (lane >> 4) * 16;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    // rows and columns that do not exist repeat the last one: their sums are not stored
+    const char *b = (const char *)p.b + (q.group * p.b_group + min(q.j0 + row, p.J - 1) * p.b_j) * ES + part;
+    const char *a[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) a[t] = (const char *)p.a + min(q.i0 + t * 16 + row, q.i1 - 1) * p.a_i * ES + part;
+    const uint64_t bytes = (uint64_t)(q.c1 - q.c0) * ES;
+    const uint32_t steps = (uint32_t)((bytes + 63) / 64), whole = (uint32_t)(bytes / 64);
+    uint32_t s = (uint32_t)((uint64_t)steps * wave / W);
+    const uint32_t s1 = (uint32_t)((uint64_t)steps * (wave + 1) / W);
+    f32x4 acc[RT] = {};
+    for (; s + U <= min(s1, whole); s += U) {
+        u32x4 vb[U], va[U][RT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) vb[u] = *(const u32x4 *)(b + (uint64_t)(s + u) * 64);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) va[u][t] = *(const u32x4 *)(a[t] + (uint64_t)(s + u) * 64);
+#pragma unroll
+        for (int u = 0; u < U; ++u) few_multiply<RT, E4M3>(acc, vb[u], va[u]);
+    }
+    for (; s < s1; ++s) {
+        u32x4 vb = {}, va[RT] = {};
+        if ((uint64_t)s * 64 + part < bytes) {          // a whole chunk, or none of it
+            vb = *(const u32x4 *)(b + (uint64_t)s * 64);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) va[t] = *(const u32x4 *)(a[t] + (uint64_t)s * 64);
+        }
+        few_multiply<RT, E4M3>(acc, vb, va);
+    }
+    // the accumulators hold row lane % 16, columns 4 (lane / 16) + r
+#pragma unroll
+    for (int t = 0; t < RT; ++t) *(f32x4 *)(sums + (wave * (RT * 16) + t * 16 + row) * 20 + (lane >> 4) * 4) = acc[t];
+    __syncthreads();
+    switch (p.act) {
+        case EC_ACT_GELU: few_finish<RT, EC_ACT_GELU>(p, q, sums, W); break;
+        case EC_ACT_SILU: few_finish<RT, EC_ACT_SILU>(p, q, sums, W); break;
+        case EC_ACT_RELU: few_finish<RT, EC_ACT_RELU>(p, q, sums, W); break;
+        default: few_finish<RT, EC_ACT_NONE>(p, q, sums, W);
+    }
 }
 
 // ------------------------------------------------------- rows made readable
@@ -519,16 +682,28 @@ __global__ __launch_bounds__(256) void column_join_kernel(const float *in, float
 
 // ---------------------------------------------------------------------- plan
 
-using Wide = Shape<128, 256, 2, 2, 3, 2>;
+using Huge = Shape<256, 256, 2, 4, 4, 1>;
 using Even = Shape<128, 128, 2, 2, 4, 2>;
-using Small = Shape<64, 64, 2, 2, 6, 2>;
-using Flat = Shape<32, 128, 1, 4, 6, 2>;
+using Small = Shape<64, 64, 2, 2, 6, 3>;
 
-enum ShapeId { kWide, kEven, kSmall, kFlat };
-constexpr uint32_t kTI[] = {128, 128, 64, 32}, kTJ[] = {256, 128, 64, 128};
+enum ShapeId { kHuge, kEven, kSmall, kFew };
+
+// What a plan's time is made of, measured on whole runs (us): a stage of one
+// workgroup alone on its CU, a stage per workgroup where every CU is full, and
+// what a workgroup costs besides its stages; bf16 and e4m3.  The full rates
+// are 1.07, 0.87 and 0.51 PFLOP/s in bf16.
+struct ShapeCost {
+    uint32_t TI, TJ, per_cu;
+    float alone[2], full[2], fixed;
+};
+constexpr ShapeCost kCost[] = {{256, 256, 1, {0.55f, 1.1f}, {0.86f, 1.5f}, 10.0f},
+                               {128, 128, 2, {0.25f, 0.43f}, {0.31f, 0.45f}, 5.0f},
+                               {64, 64, 3, {0.17f, 0.28f}, {0.133f, 0.18f}, 6.0f}};
+constexpr uint64_t kCUs = 256;
 
 struct Plan {
     uint32_t shape, splits, tiles_i, tiles_j;
+    uint32_t row_tiles, waves;              // kFew
     uint64_t blocks;
     uint32_t a_pitch, b_pitch;              // elements; 0: read in place
     uint64_t a_at, b_at, partial_at, bytes; // workspace
@@ -564,23 +739,52 @@ Plan make_plan(const ProductArgs &a) {
             at += round_up((outer_a ? 1 : groups) * b_rows * q.b_pitch * es, 256);
         }
     }
-    const uint64_t rows = ragged ? ceil_div(a.I, groups) : a.I; // typical of a row range
-    const uint64_t wide = ceil_div(rows, 128) * ceil_div(a.J, 256) * groups;
-    q.shape = rows <= 32 ? kFlat : wide >= 256 ? kWide : ceil_div(rows, 128) * ceil_div(a.J, 128) * groups >= 128 ? kEven : kSmall;
-    const uint32_t TI = kTI[q.shape], TJ = kTJ[q.shape];
-    uint64_t ti = ceil_div(a.I, TI);
-    if (ragged) ti = a.I / TI + (a.I < groups + 2 ? a.I : groups + 2);
+    q.splits = 1;
+    // Row tiles of a ragged product: at most one begun a group besides the whole ones.
+    const auto most_tiles = [&](uint64_t tile) {
+        return ragged ? a.I / tile + (a.I < groups + 2 ? a.I : groups + 2) : ceil_div(a.I, tile);
+    };
+    // Few rows a group, forward: one row by 16384 x 2048 weights takes 13.5 us
+    // so, 20 us in tiles with a split contraction and its join.
+    const uint64_t rows = ragged ? ceil_div(a.I, groups) : a.I;
+    if (a.op == EC_LINEAR_FORWARD && rows <= 32) {
+        q.shape = kFew;
+        q.row_tiles = rows <= 16 ? 1 : 2;
+        q.tiles_i = (uint32_t)most_tiles(16 * q.row_tiles);
+        q.tiles_j = (uint32_t)ceil_div(a.J, 16);
+        // Waves that share a contraction: as many as give every CU 16, with 8 steps of 64 bytes each.
+        const uint64_t tiles = ragged ? groups * q.tiles_j : (uint64_t)q.tiles_i * q.tiles_j;
+        const uint64_t want = ceil_div(16 * kCUs, tiles), most = ceil_div((uint64_t)a.C * es, 512);
+        const uint64_t w = want < most ? want : most;
+        q.waves = w <= 4 ? 4 : w <= 8 ? 8 : 16;
+        q.blocks = (uint64_t)q.tiles_i * q.tiles_j;
+        q.bytes = at;
+        return q;
+    }
+    // The tiles and the number of splits with the least time.
+    const uint64_t stages = ceil_div((outer_a ? ceil_div(a.C, groups) : (uint64_t)a.C) * es, kStageBytes);
+    float best = 0.0f;
+    for (uint32_t id = kHuge; id <= kSmall; ++id) {
+        const ShapeCost &c = kCost[id];
+        const uint64_t ti = ragged ? a.I / c.TI + (groups + 1) / 2 : ceil_div(a.I, c.TI);
+        const uint64_t tiles = ti * ceil_div(a.J, c.TJ) * (outer_a ? groups : 1);
+        for (uint32_t n = 1; n == 1 || (!a.groups && n <= 32 && stages / n >= 8); n *= 2) {
+            const uint64_t rounds = ceil_div(tiles * n, kCUs * c.per_cu), each = ceil_div(stages, n);
+            const float alone = rounds * c.alone[es == 1], full = ceil_div(tiles * n, kCUs) * c.full[es == 1];
+            float t = (alone > full ? alone : full) * each + c.fixed * rounds;
+            if (n > 1) t += 4.0f + (float)n * a.I * a.J * 1e-6f;      // the partial sums' bytes at 4 TB/s
+            if (!best || t < best) {
+                best = t;
+                q.shape = id;
+                q.splits = n;
+            }
+        }
+    }
+    const uint32_t TI = kCost[q.shape].TI, TJ = kCost[q.shape].TJ;
+    const uint64_t ti = most_tiles(TI);
     q.tiles_i = (uint32_t)ti;
     q.tiles_j = (uint32_t)ceil_div(a.J, TJ);
-    q.splits = 1;
     q.blocks = ti * q.tiles_j * (outer_a ? groups : 1);
-    if (!a.groups) {
-        const uint64_t stages = ceil_div((uint64_t)a.C * es, kStageBytes);
-        uint64_t s = q.blocks ? 512 / q.blocks : 1;
-        if (s > stages / 8) s = stages / 8;
-        if (s > 32) s = 32;
-        if (s > 1) q.splits = (uint32_t)s;
-    }
     q.partial_at = at;
     if (q.splits > 1) {
         at += q.splits * q.blocks * TI * TJ * 4;
@@ -592,8 +796,8 @@ Plan make_plan(const ProductArgs &a) {
 
 template <class T, int OP, bool E4M3>
 void launch_shape(const ProductArgs &a, const Plan &q, hipStream_t s) {
-    product_kernel<T, OP, E4M3><<<(uint32_t)q.blocks, 256, 0, s>>>(a);
-    if (q.splits > 1) join_kernel<T, OP><<<q.tiles_i * q.tiles_j * T::NI * T::NJ, 256, 0, s>>>(a);
+    product_kernel<T, OP, E4M3><<<(uint32_t)q.blocks, T::THREADS, 0, s>>>(a);
+    if (q.splits > 1) join_kernel<T, OP><<<q.tiles_i * q.tiles_j * T::NI * T::NJ, T::THREADS, 0, s>>>(a);
 }
 
 template <class T>
@@ -606,6 +810,17 @@ void launch_op(const ProductArgs &a, const Plan &q, hipStream_t s) {
         launch_shape<T, EC_LINEAR_FORWARD, true>(a, q, s);
     else
         launch_shape<T, EC_LINEAR_FORWARD, false>(a, q, s);
+}
+
+template <int RT, bool E4M3>
+void launch_few(const ProductArgs &a, const Plan &q, hipStream_t s) {
+    const uint32_t n = (uint32_t)q.blocks;
+    if (q.waves == 4)
+        few_rows_kernel<RT, 4, E4M3><<<n, 256, 0, s>>>(a);
+    else if (q.waves == 8)
+        few_rows_kernel<RT, 8, E4M3><<<n, 512, 0, s>>>(a);
+    else
+        few_rows_kernel<RT, 16, E4M3><<<n, 1024, 0, s>>>(a);
 }
 
 hipError_t copy_rows(const void *p, uint64_t stride, uint64_t group_stride, uint64_t groups, uint64_t rows,
@@ -658,10 +873,14 @@ hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s) {
     a.splits = q.splits;
     a.partial = (float *)(ws + q.partial_at);
     switch (q.shape) {
-        case kWide: launch_op<Wide>(a, q, s); break;
+        case kHuge: launch_op<Huge>(a, q, s); break;
         case kEven: launch_op<Even>(a, q, s); break;
         case kSmall: launch_op<Small>(a, q, s); break;
-        default: launch_op<Flat>(a, q, s);
+        default:
+            if (a.dtype == EC_E4M3)
+                q.row_tiles == 1 ? launch_few<1, true>(a, q, s) : launch_few<2, true>(a, q, s);
+            else
+                q.row_tiles == 1 ? launch_few<1, false>(a, q, s) : launch_few<2, false>(a, q, s);
     }
     return hipGetLastError();
 }
