@@ -30,6 +30,37 @@ __device__ __forceinline__ void load_chunk(const void *p, uint32_t dtype, uint64
     }
 }
 
+// A chunk on its way: as it lies in memory where it is whole, so that a row
+// loaded ahead takes half the registers in bf16.
+template <bool F32, bool WHOLE>
+struct Chunk {
+    static constexpr bool kRaw = WHOLE && !F32;
+    float v[kRaw ? 1 : 8];
+    u32x4 raw;
+
+    __device__ __forceinline__ void load(const void *p, uint64_t at, uint32_t left) {
+        if constexpr (kRaw) {
+            raw = u32x4{0, 0, 0, 0};
+            if (left) raw = ((const AnyU32x4 *)((const uint16_t *)p + at))->v;
+        } else {
+            load_chunk<WHOLE>(p, F32 ? EC_FP32 : EC_BF16, at, left, v);
+        }
+    }
+
+    __device__ __forceinline__ void get(float *o) const {
+        if constexpr (kRaw) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                o[2 * q] = __uint_as_float(raw[q] << 16);
+                o[2 * q + 1] = __uint_as_float(raw[q] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = v[q];
+        }
+    }
+};
+
 // weight or bias; `none` where there is none
 template <bool WHOLE>
 __device__ __forceinline__ void load_param(const void *p, uint32_t dtype, uint32_t c, uint32_t left, float none,
@@ -71,19 +102,38 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float *sh) {
 template <bool F32, bool WHOLE, int BLOCK, int THREADS, int V>
 __global__ __launch_bounds__(BLOCK) void norm_kernel(NormArgs p) {
     constexpr int kRows = BLOCK / THREADS;                          // a workgroup's rows at a time
-    constexpr uint32_t kType = F32 ? EC_FP32 : EC_BF16;
     __shared__ float sh[16];
     const uint32_t t = threadIdx.x % THREADS;
     const float scale = p.out_scale ? *p.out_scale : 1.0f, cols = (float)p.cols;
-    for (uint64_t first = (uint64_t)blockIdx.x * kRows; first < p.rows; first += (uint64_t)gridDim.x * kRows) {
+    // weight and bias stay in registers over the rows, and the next row is
+    // loaded while this one is worked on
+    constexpr bool kKeep = V <= 4;
+    float w[kKeep ? V : 1][8], b[kKeep ? V : 1][8];
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t c = 8 * (v * THREADS + t), left = left_of<WHOLE>(p.cols, c);
+            load_param<WHOLE>(p.weight, p.w_dtype, c, left, 1.0f, w[v]);
+            load_param<WHOLE>(p.bias, p.w_dtype, c, left, 0.0f, b[v]);
+        }
+    }
+    Chunk<F32, WHOLE> ahead[V];
+    const auto load = [&](uint64_t row) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t c = 8 * (v * THREADS + t);
+            ahead[v].load(p.x, row * p.x_stride + c, row < p.rows ? left_of<WHOLE>(p.cols, c) : 0);
+        }
+    };
+    const uint64_t step = (uint64_t)gridDim.x * kRows;
+    load((uint64_t)blockIdx.x * kRows + threadIdx.x / THREADS);
+    for (uint64_t first = (uint64_t)blockIdx.x * kRows; first < p.rows; first += step) {
         const uint64_t row = first + threadIdx.x / THREADS;
         const bool in = row < p.rows;
         float x[V][8], s[1] = {0.0f};
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const uint32_t c = 8 * (v * THREADS + t);
-            load_chunk<WHOLE>(p.x, kType, row * p.x_stride + c, in ? left_of<WHOLE>(p.cols, c) : 0, x[v]);
-        }
+        for (int v = 0; v < V; ++v) ahead[v].get(x[v]);
+        if (first + step < p.rows) load(row + step);
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -111,11 +161,13 @@ __global__ __launch_bounds__(BLOCK) void norm_kernel(NormArgs p) {
         for (int v = 0; v < V; ++v) {
             const uint32_t c = 8 * (v * THREADS + t), left = left_of<WHOLE>(p.cols, c);
             if (!left) break;
-            float w[8], b[8];
-            load_param<WHOLE>(p.weight, p.w_dtype, c, left, 1.0f, w);
-            load_param<WHOLE>(p.bias, p.w_dtype, c, left, 0.0f, b);
+            const int k = kKeep ? v : 0;
+            if constexpr (!kKeep) {
+                load_param<WHOLE>(p.weight, p.w_dtype, c, left, 1.0f, w[0]);
+                load_param<WHOLE>(p.bias, p.w_dtype, c, left, 0.0f, b[0]);
+            }
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[v][q] = (x[v][q] * rstd * w[q] + b[q]) * scale;
+            for (int q = 0; q < 8; ++q) x[v][q] = (x[v][q] * rstd * w[k][q] + b[k][q]) * scale;
             store8(p.y, p.out_dtype, row * p.y_stride + c, left, x[v]);
         }
     }
@@ -140,17 +192,36 @@ __global__ __launch_bounds__(512) void norm_grad_kernel(NormGradArgs p) {
         const uint32_t c = first + 8 * (v * THREADS + t);
         load_param<WHOLE>(p.weight, p.w_dtype, c, left_of<WHOLE>(p.cols, c), 1.0f, w[v]);
     }
-    for (uint64_t base = (uint64_t)blockIdx.x * kRows; base < p.rows; base += (uint64_t)gridDim.x * kRows) {
-        const uint64_t row = base + r0;
+    // the next row is loaded while this one is worked on
+    Chunk<F32, WHOLE> nx[V], nd[V], nr[V];
+    float nmean, nrstd;
+    const auto load = [&](uint64_t row) {
         const bool in = row < p.rows;
-        const float mean = in ? p.mean[row] : 0.0f, rstd = in ? p.rstd[row] : 0.0f;
-        float h[V][8], dy[V][8], s[2] = {0.0f, 0.0f};
+        nmean = in ? p.mean[row] : 0.0f;
+        nrstd = in ? p.rstd[row] : 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const uint32_t c = first + 8 * (v * THREADS + t), left = in ? left_of<WHOLE>(p.cols, c) : 0;
-            load_chunk<WHOLE>(p.x, kType, row * p.x_stride + c, left, h[v]);
-            load_chunk<WHOLE>(p.dy, kType, row * p.dy_stride + c, left, dy[v]);
+            nx[v].load(p.x, row * p.x_stride + c, left);
+            nd[v].load(p.dy, row * p.dy_stride + c, left);
+            nr[v].load(p.dres, row * p.dres_stride + c, p.dres && p.dx ? left : 0);
         }
+    };
+    const uint64_t step = (uint64_t)gridDim.x * kRows;
+    load((uint64_t)blockIdx.x * kRows + r0);
+    for (uint64_t base = (uint64_t)blockIdx.x * kRows; base < p.rows; base += step) {
+        const uint64_t row = base + r0;
+        const bool in = row < p.rows;
+        const float mean = nmean, rstd = nrstd;
+        float h[V][8], dy[V][8], s[2] = {0.0f, 0.0f};
+        Chunk<F32, WHOLE> dres[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            nx[v].get(h[v]);
+            nd[v].get(dy[v]);
+            dres[v] = nr[v];
+        }
+        if (base + step < p.rows) load(row + step);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const uint32_t left = left_of<WHOLE>(p.cols, first + 8 * (v * THREADS + t));
@@ -188,8 +259,8 @@ __global__ __launch_bounds__(512) void norm_grad_kernel(NormGradArgs p) {
         for (int v = 0; v < V; ++v) {
             const uint32_t c = first + 8 * (v * THREADS + t), left = left_of<WHOLE>(p.cols, c);
             if (!left) break;
-            float o[8], res[8] = {};
-            if (p.dres) load_chunk<WHOLE>(p.dres, kType, row * p.dres_stride + c, left, res);
+            float o[8], res[8];
+            dres[v].get(res);
 #pragma unroll
             for (int q = 0; q < 8; ++q) o[q] = rstd * (dy[v][q] * w[v][q] - mt - h[v][q] * mth) + res[q];
             store8(p.dx, kType, row * p.dx_stride + c, left, o);
@@ -237,6 +308,7 @@ __global__ __launch_bounds__(256) void norm_grad_sum_kernel(NormGradArgs p) {
     const uint64_t c = (uint64_t)blockIdx.x * 16 + x, n = 2 * (uint64_t)p.cols;
     float s = 0.0f;
     if (c < n)
+#pragma unroll 8                            // loads of eight parts on the way
         for (uint32_t q = y; q < p.parts; q += 16) s += p.partial[q * n + c];
     sh[y][x] = s;
     __syncthreads();
@@ -253,7 +325,9 @@ template <bool F32, int BLOCK, int THREADS, int V>
 void run_norm(const NormArgs &a, hipStream_t s) {
     constexpr int kRows = BLOCK / THREADS;
     const uint64_t need = (a.rows + kRows - 1) / kRows;
-    const uint32_t blocks = (uint32_t)(need < 65536 ? need : 65536);
+    // as many workgroups as run at a time, 16 waves a CU, each with several rows
+    const uint64_t most = 256 * 1024 / BLOCK;
+    const uint32_t blocks = (uint32_t)(need < most ? need : most);
     if (a.cols % 8 == 0)
         norm_kernel<F32, true, BLOCK, THREADS, V><<<blocks, BLOCK, 0, s>>>(a);
     else

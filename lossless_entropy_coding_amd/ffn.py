@@ -50,9 +50,15 @@ class _LinearArgs(ctypes.Structure):
     ]
 
 
+_package = None
+
+
 def _ec():
-    import lossless_entropy_coding_amd as ec
-    return ec
+    global _package
+    if _package is None:
+        import lossless_entropy_coding_amd
+        _package = lossless_entropy_coding_amd
+    return _package
 
 
 def _error(text: str):
@@ -61,6 +67,12 @@ def _error(text: str):
 
 def _matrix(t, name: str, rows: int, cols: int, dtypes, device=None):
     """Checks a 2-D CUDA tensor with contiguous rows; returns its row stride."""
+    # one pass of cheap checks for what is in order: a call on one token takes as long as the host needs for it
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.shape == (rows, cols) and t.dtype in dtypes \
+            and (device is None or t.device == device):
+        s, one = t.stride()
+        if one == 1 and s >= cols:
+            return s
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
         _error("%s must be a 2-D CUDA tensor" % name)
     if t.dtype not in dtypes:
@@ -84,6 +96,9 @@ def _row_stride(t, name: str) -> int:
 
 
 def _vector(t, name: str, shapes, dtypes, device):
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device and t.shape in shapes \
+            and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
         _error("%s must be a contiguous %s tensor on %s" % (name, " or ".join(str(d) for d in dtypes), device))
     if tuple(t.shape) not in shapes:
@@ -94,6 +109,10 @@ def _act(act) -> int:
     if act not in _ACTS:
         _error("act must be None, 'gelu', 'silu' or 'relu', not %r" % (act,))
     return _ACTS[act]
+
+
+# straight from torch's C layer, a quarter of the time (public API as the fallback)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _empty(shape, dtype, device):
@@ -110,7 +129,7 @@ def _placed(fn):
         if stream is not None:
             with torch.cuda.stream(stream):
                 return call(t, *args, **kw)
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
             with torch.cuda.device(t.device):
                 return fn(t, *args, **kw)
         return fn(t, *args, **kw)
@@ -131,6 +150,10 @@ def _call(name: str, args: _LinearArgs, op: int, device):
 def _weights(w, name: str, offsets, dtypes):
     """(groups, n, k, row stride, group stride) of [n, k] or [groups, n, k] weights."""
     grouped = offsets is not None
+    if not grouped and isinstance(w, torch.Tensor) and w.is_cuda and w.dim() == 2 and w.dtype in dtypes:
+        (n, k), (s, one) = w.shape, w.stride()
+        if one == 1 and s >= k:
+            return 0, n, k, s, 0
     if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dim() != (3 if grouped else 2):
         _error("%s must be a %d-D CUDA tensor" % (name, 3 if grouped else 2))
     if w.dtype not in dtypes:
@@ -193,10 +216,11 @@ def _forward(x, w, offsets, bias, act, residual, x_scale, w_scale, out_scale, ou
             out_dtype = torch.bfloat16
         if out_dtype not in _DTYPES:
             _error("out_dtype must be bfloat16, float32, float8_e4m3fn or uint8 (e4m3 bytes), not %s" % out_dtype)
-        out = _empty((m, n), out_dtype, dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        _error("out is %s, out_dtype %s" % (out.dtype, out_dtype))
-    a.y_stride = _matrix(out, "out", m, n, tuple(_DTYPES), dev)
+        out, a.y_stride = _empty((m, n), out_dtype, dev), n
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            _error("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        a.y_stride = _matrix(out, "out", m, n, _DTYPES, dev)
     a.y, a.out_dtype = out.data_ptr(), _DTYPES[out.dtype]
     if out_scale is not None:
         if a.out_dtype != _E4M3:
@@ -205,8 +229,9 @@ def _forward(x, w, offsets, bias, act, residual, x_scale, w_scale, out_scale, ou
         a.out_scale = out_scale.data_ptr()
     if save_preact or preact is not None:
         if preact is None:
-            preact = _empty((m, n), torch.bfloat16, dev)
-        a.preact_stride = _matrix(preact, "preact", m, n, (torch.bfloat16,), dev)
+            preact, a.preact_stride = _empty((m, n), torch.bfloat16, dev), n
+        else:
+            a.preact_stride = _matrix(preact, "preact", m, n, (torch.bfloat16,), dev)
         a.preact = preact.data_ptr()
     _call("linear_forward", a, _FORWARD, dev)
     return out if preact is None else (out, preact)
@@ -269,8 +294,10 @@ def _backward(dy, x, w, offsets, preact, act, need_dx, need_dw, need_db, dw_dtyp
                 _error("preact (the activation's input) is needed for the gradient through act")
             a.preact_stride, a.preact = _matrix(preact, "preact", m, k, bf, dev), preact.data_ptr()
         if dx is None:
-            dx = _empty((m, k), torch.bfloat16, dev)
-        a.dx_stride, a.dx = _matrix(dx, "dx", m, k, bf, dev), dx.data_ptr()
+            dx, a.dx_stride = _empty((m, k), torch.bfloat16, dev), k
+        else:
+            a.dx_stride = _matrix(dx, "dx", m, k, bf, dev)
+        a.dx = dx.data_ptr()
         _call("linear_grad_input", a, _GRAD_INPUT, dev)
     if need_dw or need_db:
         if need_dw:
@@ -288,7 +315,8 @@ def _backward(dy, x, w, offsets, preact, act, need_dx, need_dw, need_db, dw_dtyp
         if need_db:
             if db is None:
                 db = _empty(per + (n,), torch.float32, dev)
-            _vector(db, "db", (per + (n,),), (torch.float32,), dev)
+            else:
+                _vector(db, "db", (per + (n,),), (torch.float32,), dev)
             a.db = db.data_ptr()
         _call("linear_grad_weight", a, _GRAD_WEIGHT, dev)
     return dx, dw, db
@@ -358,19 +386,20 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, out_dtype=None, 
         out_dtype = x.dtype if out_dtype is None else out_dtype
         if out_dtype not in _DTYPES:
             _error("out_dtype must be bfloat16, float32, float8_e4m3fn or uint8 (e4m3 bytes), not %s" % out_dtype)
-        out = _empty((rows, cols), out_dtype, dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        _error("out is %s, out_dtype %s" % (out.dtype, out_dtype))
-    ys = _matrix(out, "out", rows, cols, tuple(_DTYPES), dev)
+        out, ys = _empty((rows, cols), out_dtype, dev), cols
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            _error("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        ys = _matrix(out, "out", rows, cols, _DTYPES, dev)
     if out_scale is not None:
         if _DTYPES[out.dtype] != _E4M3:
             _error("out_scale goes with an e4m3 output")
         _vector(out_scale, "out_scale", ((1,),), (torch.float32,), dev)
     if mean is None and rstd is None:
-        stats = _empty((2, rows), torch.float32, dev)
-        mean, rstd = stats[0], stats[1]
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _vector(t, name, ((rows,),), (torch.float32,), dev)
+        mean, rstd = _empty((rows,), torch.float32, dev), _empty((rows,), torch.float32, dev)
+    else:
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            _vector(t, name, ((rows,),), (torch.float32,), dev)
     ec._check(ec.lib().layer_norm_forward(x.data_ptr(), _DTYPES[x.dtype], rows, cols, xs, _ptr(weight), _ptr(bias),
                                           w_dtype, float(eps), out.data_ptr(), _DTYPES[out.dtype], ys,
                                           _ptr(out_scale), mean.data_ptr(), rstd.data_ptr(), ec._stream(None)),
@@ -404,14 +433,20 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, residual_grad=None, n
         need_dbias or dbias is not None
     xds = 0
     if need_dx:
-        dx = _empty((rows, cols), x.dtype, dev) if dx is None else dx
-        xds = _matrix(dx, "dx", rows, cols, same, dev)
+        if dx is None:
+            dx, xds = _empty((rows, cols), x.dtype, dev), cols
+        else:
+            xds = _matrix(dx, "dx", rows, cols, same, dev)
     if need_dweight:
-        dweight = _empty((cols,), torch.float32, dev) if dweight is None else dweight
-        _vector(dweight, "dweight", ((cols,),), (torch.float32,), dev)
+        if dweight is None:
+            dweight = _empty((cols,), torch.float32, dev)
+        else:
+            _vector(dweight, "dweight", ((cols,),), (torch.float32,), dev)
     if need_dbias:
-        dbias = _empty((cols,), torch.float32, dev) if dbias is None else dbias
-        _vector(dbias, "dbias", ((cols,),), (torch.float32,), dev)
+        if dbias is None:
+            dbias = _empty((cols,), torch.float32, dev)
+        else:
+            _vector(dbias, "dbias", ((cols,),), (torch.float32,), dev)
     L = ec.lib()
     ws, need = None, 0
     if need_dweight or need_dbias:
