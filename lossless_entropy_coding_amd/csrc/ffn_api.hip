@@ -176,8 +176,7 @@ ColumnSumArgs column_sum(const ec_linear_args *a) {
     return c;
 }
 
-int run_product(const ec_linear_args *a, uint32_t op, hipStream_t stream) {
-    const ProductArgs p = product(a, op);
+int run_product(const ec_linear_args *a, const ProductArgs &p, hipStream_t stream) {
     const uint64_t need = product_workspace(p);
     if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;
     return hip_code(launch_product(p, a->d_workspace, stream));
@@ -188,7 +187,8 @@ int run_product(const ec_linear_args *a, uint32_t op, hipStream_t stream) {
 uint64_t linear_workspace_bytes(const ec_linear_args *a, uint32_t op) {
     if (check(a, op)) return 0;
     uint64_t need = has_product(a, op) ? product_workspace(product(a, op)) : 0;
-    if (op == EC_LINEAR_GRAD_WEIGHT && a->d_db) {   // one after the other, in the same memory
+    if (op == EC_LINEAR_GRAD_WEIGHT && a->d_db && !(a->d_dw && product_sums_columns(product(a, op)))) {
+        // one after the other, in the same memory
         const uint64_t sums = column_sum_workspace(column_sum(a));
         need = sums > need ? sums : need;
     }
@@ -197,18 +197,23 @@ uint64_t linear_workspace_bytes(const ec_linear_args *a, uint32_t op) {
 
 int linear_forward(const ec_linear_args *a, hipStream_t stream) {
     const int rc = check_forward(a);
-    return rc ? rc : run_product(a, EC_LINEAR_FORWARD, stream);
+    return rc ? rc : run_product(a, product(a, EC_LINEAR_FORWARD), stream);
 }
 
 int linear_grad_input(const ec_linear_args *a, hipStream_t stream) {
     const int rc = check_grad_input(a);
-    return rc ? rc : run_product(a, EC_LINEAR_GRAD_INPUT, stream);
+    return rc ? rc : run_product(a, product(a, EC_LINEAR_GRAD_INPUT), stream);
 }
 
 int linear_grad_weight(const ec_linear_args *a, hipStream_t stream) {
     int rc = check_grad_weight(a);
     if (rc) return rc;
-    if (a->d_dw && (rc = run_product(a, EC_LINEAR_GRAD_WEIGHT, stream))) return rc;
+    if (a->d_dw) {
+        ProductArgs p = product(a, EC_LINEAR_GRAD_WEIGHT);
+        const bool both = a->d_db && product_sums_columns(p);
+        if (both) p.db = a->d_db;
+        if ((rc = run_product(a, p, stream)) || both) return rc;
+    }
     if (!a->d_db) return EC_OK;
     const ColumnSumArgs c = column_sum(a);
     const uint64_t need = column_sum_workspace(c);

@@ -50,6 +50,7 @@ struct ProductArgs {
     uint64_t out_stride, out_group;        // out_group: elements between experts' dw
     uint16_t *preact;                      // written (forward) or read (grad input)
     uint64_t preact_stride;
+    float *db;                             // grad weight: [groups][I] sums of A over the contraction, or null
     // filled in by the plan
     uint32_t tiles_i, tiles_j, splits;
     float *partial;                        // [splits][tile][TI * TJ] when splits > 1
@@ -65,6 +66,7 @@ struct ColumnSumArgs {                     // db
 };
 
 uint64_t product_workspace(const ProductArgs &a);
+bool product_sums_columns(const ProductArgs &a);    // whether the product can write db as well
 hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s);
 uint64_t column_sum_workspace(const ColumnSumArgs &a);
 hipError_t launch_column_sum(const ColumnSumArgs &a, float *workspace, hipStream_t s);

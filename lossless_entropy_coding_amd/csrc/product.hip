@@ -337,7 +337,18 @@ __device__ __forceinline__ Place find_place(const ProductArgs &p, uint32_t block
     return q;
 }
 
-template <class T, int OP, bool E4M3>
+__device__ __forceinline__ float sum8(const u32x4 &w) {
+    float s[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) s[d] = __uint_as_float(w[d] << 16) + __uint_as_float(w[d] & 0xFFFF0000u);
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// SUM (grad weight by group): db too.  The branch costs the loop a tenth, so
+// it is not in the kernel of one dense product, whose dy is little to read
+// again (2048 x 16384 x 2048: 127 us and 10 us for the sums, 141 us together);
+// 16 groups of 8192 rows by 2048 columns: 69 us and 16 us, 76 us together.
+template <class T, int OP, bool E4M3, bool SUM>
 __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
     constexpr bool kOuterA = OP == EC_LINEAR_GRAD_WEIGHT, kOuterB = OP != EC_LINEAR_FORWARD;
     constexpr int kES = E4M3 ? 1 : 2, kDepth = kStageBytes / kES;
@@ -370,6 +381,10 @@ __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
         for (int y = 0; y < NJ; ++y)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[x][y][r] = 0.0f;
+    // db, the sum of A over the contraction: the first tile of a row of tiles
+    // adds up its fragments, a wave those of one of its NI tiles of 32 rows
+    // (the waves side by side hold the same ones).
+    float db = 0.0f;
 
     if (c1 > c0) {
         const uint32_t n = (c1 - c0 + kDepth - 1) / kDepth;
@@ -425,6 +440,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
         // The loads are spread over the products of stage k (a wave whose load
         // finds the queue full issues no products either), the reads over
         // their first half, so that the wait for the last one is short.
+        const bool sum = SUM && q.j0 == 0;
         const auto step = [&](int now) {
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * kLoads) : "memory");
             __builtin_amdgcn_s_barrier();
@@ -441,6 +457,19 @@ __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
                 for (int k = 0; k < kLoads; ++k)
                     if (k >= g * kLoads / G && k < (g + 1) * kLoads / G) load(k);
             });
+            if constexpr (SUM) {
+                if (sum) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        u32x4 f = af[now][0][s];
+#pragma unroll
+                        for (int x = 1; x < NI; ++x)
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) f[d] = wave % T::WJ == (uint32_t)x ? af[now][x][s][d] : f[d];
+                        db += sum8(f);
+                    }
+                }
+            }
         };
         for (uint32_t k = 0;;) {
             step(0);
@@ -452,6 +481,12 @@ __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
 
+    if constexpr (SUM) {
+        // The lane's two halves of the contraction; row lane % 32 of the wave's tile x.
+        db += __shfl_xor(db, 32);
+        const uint32_t x = wave % T::WJ, i = q.i0 + wi + x * 32 + lane;
+        if (q.j0 == 0 && x < (uint32_t)NI && lane < 32 && i < q.i1) p.db[(uint64_t)q.group * p.I + i] = db;
+    }
     if (p.splits > 1) {
         float *o = p.partial + ((uint64_t)q.split * (p.tiles_i * p.tiles_j) + q.tile) * (T::TI * T::TJ);
         o += wave * (NI * NJ * 1024) + lane * 4;
@@ -510,6 +545,21 @@ struct Few {
     static constexpr int kAtOnce = 8;                   // loads of B on the way in a lane
 };
 
+struct __attribute__((packed, aligned(1))) AnyByteU32x4 { u32x4 v; };
+
+// The first n < 16 / ES values at p, and zeros.
+template <int ES>
+__device__ __forceinline__ u32x4 few_values(const char *p, uint32_t n) {
+    u32x4 w = {};
+    for (uint32_t k = 0; k < n; ++k) {
+        const uint32_t v = ES == 1 ? (uint32_t)((const uint8_t *)p)[k] : (uint32_t)((const uint16_t *)p)[k];
+        const uint32_t bit = k * ES * 8;
+#pragma unroll
+        for (uint32_t d = 0; d < 4; ++d) w[d] |= d == bit / 32 ? v << (bit & 31) : 0;
+    }
+    return w;
+}
+
 template <int RT, bool E4M3>
 __device__ __forceinline__ void few_multiply(f32x4 (&acc)[RT], const u32x4 &b, const u32x4 (&a)[RT]) {
 #pragma unroll
@@ -567,20 +617,26 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(ProductArgs p) {
     for (; s + U <= min(s1, whole); s += U) {
         u32x4 vb[U], va[U][RT];
 #pragma unroll
-        for (int u = 0; u < U; ++u) vb[u] = *(const u32x4 *)(b + (uint64_t)(s + u) * 64);
+        for (int u = 0; u < U; ++u) vb[u] = ((const AnyByteU32x4 *)(b + (uint64_t)(s + u) * 64))->v;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int t = 0; t < RT; ++t) va[u][t] = *(const u32x4 *)(a[t] + (uint64_t)(s + u) * 64);
+            for (int t = 0; t < RT; ++t) va[u][t] = ((const AnyByteU32x4 *)(a[t] + (uint64_t)(s + u) * 64))->v;
 #pragma unroll
         for (int u = 0; u < U; ++u) few_multiply<RT, E4M3>(acc, vb[u], va[u]);
     }
     for (; s < s1; ++s) {
         u32x4 vb = {}, va[RT] = {};
-        if ((uint64_t)s * 64 + part < bytes) {          // a whole chunk, or none of it
-            vb = *(const u32x4 *)(b + (uint64_t)s * 64);
+        const uint64_t at = (uint64_t)s * 64 + part;
+        if (at + 16 <= bytes) {
+            vb = ((const AnyByteU32x4 *)(b + (uint64_t)s * 64))->v;
 #pragma unroll
-            for (int t = 0; t < RT; ++t) va[t] = *(const u32x4 *)(a[t] + (uint64_t)s * 64);
+            for (int t = 0; t < RT; ++t) va[t] = ((const AnyByteU32x4 *)(a[t] + (uint64_t)s * 64))->v;
+        } else if (at < bytes) {                        // the row's last values
+            const uint32_t n = (uint32_t)(bytes - at) / ES;
+            vb = few_values<ES>(b + (uint64_t)s * 64, n);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) va[t] = few_values<ES>(a[t] + (uint64_t)s * 64, n);
         }
         few_multiply<RT, E4M3>(acc, vb, va);
     }
@@ -726,20 +782,6 @@ Plan make_plan(const ProductArgs &a) {
     const bool outer_a = a.op == EC_LINEAR_GRAD_WEIGHT, outer_b = a.op != EC_LINEAR_FORWARD;
     const bool ragged = a.groups && !outer_a;
     const uint64_t groups = a.groups ? a.groups : 1;
-    uint64_t at = 0;
-    if (a.C) {
-        const uint64_t a_rows = outer_a ? a.C : a.I, a_cols = outer_a ? a.I : a.C;
-        const uint64_t b_rows = outer_b ? a.C : a.J, b_cols = outer_b ? a.J : a.C;
-        if (!readable(a.a, outer_a ? a.a_c : a.a_i, 0, a_cols, es, outer_a)) {
-            q.a_pitch = (uint32_t)round_up(a_cols, 16 / es);
-            at += round_up(a_rows * q.a_pitch * es, 256);
-        }
-        q.b_at = at;
-        if (!readable(a.b, outer_b ? a.b_c : a.b_j, outer_a ? 0 : a.b_group, b_cols, es, outer_b)) {
-            q.b_pitch = (uint32_t)round_up(b_cols, 16 / es);
-            at += round_up((outer_a ? 1 : groups) * b_rows * q.b_pitch * es, 256);
-        }
-    }
     q.splits = 1;
     // Row tiles of a ragged product: at most one begun a group besides the whole ones.
     const auto most_tiles = [&](uint64_t tile) {
@@ -759,9 +801,22 @@ Plan make_plan(const ProductArgs &a) {
         // Waves that share a contraction: with 1024 tiles four are enough
         // (16.4 us; 16.2 with eight), with 128 eight are better (13.4, 16.1).
         q.waves = (ragged ? groups : q.tiles_i) * q.tiles_j >= 2 * kCUs ? 4 : 8;
-        q.blocks = (uint64_t)q.tiles_i * q.tiles_j;
-        q.bytes = at;
+        q.blocks = (uint64_t)q.tiles_i * q.tiles_j;     // reads rows at any address
         return q;
+    }
+    uint64_t at = 0;
+    if (a.C) {
+        const uint64_t a_rows = outer_a ? a.C : a.I, a_cols = outer_a ? a.I : a.C;
+        const uint64_t b_rows = outer_b ? a.C : a.J, b_cols = outer_b ? a.J : a.C;
+        if (!readable(a.a, outer_a ? a.a_c : a.a_i, 0, a_cols, es, outer_a)) {
+            q.a_pitch = (uint32_t)round_up(a_cols, 16 / es);
+            at += round_up(a_rows * q.a_pitch * es, 256);
+        }
+        q.b_at = at;
+        if (!readable(a.b, outer_b ? a.b_c : a.b_j, outer_a ? 0 : a.b_group, b_cols, es, outer_b)) {
+            q.b_pitch = (uint32_t)round_up(b_cols, 16 / es);
+            at += round_up((outer_a ? 1 : groups) * b_rows * q.b_pitch * es, 256);
+        }
     }
     // The tiles and the number of splits with the least time.
     const uint64_t stages = ceil_div((outer_a ? ceil_div(a.C, groups) : (uint64_t)a.C) * es, kStageBytes);
@@ -796,9 +851,9 @@ Plan make_plan(const ProductArgs &a) {
     return q;
 }
 
-template <class T, int OP, bool E4M3>
+template <class T, int OP, bool E4M3, bool SUM = false>
 void launch_shape(const ProductArgs &a, const Plan &q, hipStream_t s) {
-    product_kernel<T, OP, E4M3><<<(uint32_t)q.blocks, T::THREADS, 0, s>>>(a);
+    product_kernel<T, OP, E4M3, SUM><<<(uint32_t)q.blocks, T::THREADS, 0, s>>>(a);
     if (q.splits > 1) join_kernel<T, OP><<<q.tiles_i * q.tiles_j * T::NI * T::NJ, T::THREADS, 0, s>>>(a);
 }
 
@@ -807,7 +862,8 @@ void launch_op(const ProductArgs &a, const Plan &q, hipStream_t s) {
     if (a.op == EC_LINEAR_GRAD_INPUT)
         launch_shape<T, EC_LINEAR_GRAD_INPUT, false>(a, q, s);
     else if (a.op == EC_LINEAR_GRAD_WEIGHT)
-        launch_shape<T, EC_LINEAR_GRAD_WEIGHT, false>(a, q, s);
+        a.db ? launch_shape<T, EC_LINEAR_GRAD_WEIGHT, false, true>(a, q, s)
+             : launch_shape<T, EC_LINEAR_GRAD_WEIGHT, false>(a, q, s);
     else if (a.dtype == EC_E4M3)
         launch_shape<T, EC_LINEAR_FORWARD, true>(a, q, s);
     else
@@ -839,6 +895,10 @@ hipError_t copy_rows(const void *p, uint64_t stride, uint64_t group_stride, uint
 }
 
 }  // namespace
+
+bool product_sums_columns(const ProductArgs &a) {
+    return a.op == EC_LINEAR_GRAD_WEIGHT && a.groups && a.I && a.J;
+}
 
 uint64_t product_workspace(const ProductArgs &a) {
     if (!a.I || !a.J) return 0;
