@@ -520,7 +520,8 @@ int bf16_exp_decode(const uint8_t *d_in, uint64_t in_len, uint16_t *d_out, uint6
  * to the element's own alignment, are free; 16-byte aligned pointers with row
  * strides and row lengths that are multiples of 16 bytes are read in place,
  * any other factor of a product is first copied into the workspace (rows
- * padded to 16 bytes).  Sizes up to 2^31 - 1.
+ * padded to 16 bytes), unless a forward product has at most 32 rows (on
+ * average by group), which reads rows at any address.  Sizes up to 2^31 - 1.
  * ------------------------------------------------------------------------- */
 
 typedef enum ec_dtype {

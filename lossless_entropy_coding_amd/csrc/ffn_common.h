@@ -289,6 +289,7 @@ __device__ __forceinline__ void check_offsets(const int32_t *offsets, uint32_t g
 // ------------------------------------------------------------------- epilogue
 
 // Vectors at any address that suits their elements.
+struct __attribute__((packed, aligned(1))) AnyByteU32x4 { u32x4 v; };
 struct __attribute__((packed, aligned(2))) AnyU32x4 { u32x4 v; };
 struct __attribute__((packed, aligned(1))) AnyU32x2 { u32x2 v; };
 struct __attribute__((packed, aligned(4))) AnyF32x4 { f32x4 v; };

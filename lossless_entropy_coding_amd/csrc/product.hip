@@ -344,9 +344,9 @@ __device__ __forceinline__ float sum8(const u32x4 &w) {
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// SUM (grad weight by group): db too.  The branch costs the loop a tenth, so
-// it is not in the kernel of one dense product, whose dy is little to read
-// again (2048 x 16384 x 2048: 127 us and 10 us for the sums, 141 us together);
+// SUM (grad weight): db too.  The branch costs the loop a tenth, so it is not
+// in the kernel of a large dense product, whose dy is little to read again
+// (2048 x 16384 x 2048: 127 us and 10 us for the sums, 141 us together);
 // 16 groups of 8192 rows by 2048 columns: 69 us and 16 us, 76 us together.
 template <class T, int OP, bool E4M3, bool SUM>
 __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
@@ -545,8 +545,6 @@ struct Few {
     static constexpr int kAtOnce = 8;                   // loads of B on the way in a lane
 };
 
-struct __attribute__((packed, aligned(1))) AnyByteU32x4 { u32x4 v; };
-
 // The first n < 16 / ES values at p, and zeros.
 template <int ES>
 __device__ __forceinline__ u32x4 few_values(const char *p, uint32_t n) {
@@ -657,25 +655,46 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(ProductArgs p) {
 // The loads above take rows at 16-byte addresses whose contraction is a whole
 // number of 16-byte chunks.  Any other factor is copied first: rows padded
 // with zeros to 16 bytes, one after the other.
+struct RowCopy {
+    const void *p;
+    uint64_t stride, group_stride, total;  // elements; total: 16-byte chunks of all groups
+    uint32_t rows, cols, pitch;            // pitch of the copy's rows, elements
+    void *out;
+    uint32_t blocks;                       // 0: none
+};
+
+// Both factors in one launch: the first a.blocks workgroups copy a's.
 template <typename E>
-__global__ __launch_bounds__(256) void copy_rows_kernel(const E *p, uint64_t stride, uint64_t group_stride,
-                                                        uint32_t rows, uint32_t cols, E *out, uint32_t pitch) {
+__global__ __launch_bounds__(256) void copy_rows_kernel(RowCopy a, RowCopy b) {
     constexpr uint32_t V = 16 / sizeof(E);
-    const uint32_t chunks = pitch / V;
-    const uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    const uint64_t row = q / chunks;
-    if (row >= rows) return;
+    const bool first = blockIdx.x < a.blocks;
+    const RowCopy &k = first ? a : b;
+    const uint32_t chunks = k.pitch / V;
+    const uint64_t q = (uint64_t)(blockIdx.x - (first ? 0 : a.blocks)) * 256 + threadIdx.x;
+    if (q >= k.total) return;
+    uint64_t row, g;
+    if (k.total >> 32) {
+        row = q / chunks;
+        g = row / k.rows;
+    } else {                                // the same in short divisions
+        row = (uint32_t)q / chunks;
+        g = (uint32_t)row / k.rows;
+    }
     const uint32_t c = (uint32_t)(q - row * chunks) * V;
-    const E *in = p + blockIdx.y * group_stride + row * stride + c;
+    const E *in = (const E *)k.p + g * k.group_stride + (row - g * k.rows) * k.stride + c;
     union {
         E e[V];
         u32x4 w;
     } u;
-    u.w = u32x4{0, 0, 0, 0};
+    if (c + V <= k.cols) {
+        u.w = ((const AnyByteU32x4 *)in)->v;
+    } else {
+        u.w = u32x4{0, 0, 0, 0};
 #pragma unroll
-    for (uint32_t k = 0; k < V; ++k)
-        if (c + k < cols) u.e[k] = in[k];
-    *(u32x4 *)(out + ((uint64_t)blockIdx.y * rows + row) * pitch + c) = u.w;
+        for (uint32_t n = 0; n < V; ++n)
+            if (c + n < k.cols) u.e[n] = in[n];
+    }
+    ((u32x4 *)k.out)[q] = u.w;
 }
 
 // ---------------------------------------------------------------- column sums
@@ -879,25 +898,20 @@ void launch_few(const ProductArgs &a, const Plan &q, hipStream_t s) {
         few_rows_kernel<RT, 8, E4M3><<<n, 512, 0, s>>>(a);
 }
 
-hipError_t copy_rows(const void *p, uint64_t stride, uint64_t group_stride, uint64_t groups, uint64_t rows,
-                     uint64_t cols, uint32_t es, void *out, uint32_t pitch, hipStream_t s) {
-    if (!rows || !cols) return hipSuccess;
-    const uint64_t blocks = ceil_div(rows * (pitch * es / 16), 256);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const dim3 grid((uint32_t)blocks, (uint32_t)groups);
-    if (es == 1)
-        copy_rows_kernel<uint8_t><<<grid, 256, 0, s>>>((const uint8_t *)p, stride, group_stride, (uint32_t)rows,
-                                                       (uint32_t)cols, (uint8_t *)out, pitch);
-    else
-        copy_rows_kernel<uint16_t><<<grid, 256, 0, s>>>((const uint16_t *)p, stride, group_stride, (uint32_t)rows,
-                                                        (uint32_t)cols, (uint16_t *)out, pitch);
-    return hipGetLastError();
+RowCopy row_copy(const void *p, uint64_t stride, uint64_t group_stride, uint64_t groups, uint64_t rows, uint64_t cols,
+                 uint32_t es, void *out, uint32_t pitch) {
+    RowCopy c = {p, stride, group_stride, groups * rows * (pitch * es / 16), (uint32_t)rows, (uint32_t)cols, pitch, out, 0};
+    const uint64_t blocks = ceil_div(c.total, 256);
+    c.blocks = blocks > 0x7FFFFFFF ? 0xFFFFFFFFu : (uint32_t)blocks;
+    return c;
 }
 
 }  // namespace
 
 bool product_sums_columns(const ProductArgs &a) {
-    return a.op == EC_LINEAR_GRAD_WEIGHT && a.groups && a.I && a.J;
+    // The second launch and its join cost 8 - 10 us, the sums a tenth of the
+    // product: up to 1024 rows that is less (see product_kernel).
+    return a.op == EC_LINEAR_GRAD_WEIGHT && a.I && a.J && (a.groups || (a.C <= 1024 && make_plan(a).splits == 1));
 }
 
 uint64_t product_workspace(const ProductArgs &a) {
@@ -912,22 +926,26 @@ hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s) {
     const uint32_t es = a.dtype == EC_E4M3 ? 1 : 2;
     const bool outer_a = a.op == EC_LINEAR_GRAD_WEIGHT, outer_b = a.op != EC_LINEAR_FORWARD;
     char *ws = (char *)workspace;
+    RowCopy ca = {}, cb = {};
     if (q.a_pitch) {
         const uint64_t rows = outer_a ? a.C : a.I, cols = outer_a ? a.I : a.C;
-        const hipError_t e = copy_rows(a.a, outer_a ? a.a_c : a.a_i, 0, 1, rows, cols, es, ws + q.a_at, q.a_pitch, s);
-        if (e != hipSuccess) return e;
+        ca = row_copy(a.a, outer_a ? a.a_c : a.a_i, 0, 1, rows, cols, es, ws + q.a_at, q.a_pitch);
         a.a = ws + q.a_at;
         (outer_a ? a.a_c : a.a_i) = q.a_pitch;
     }
     if (q.b_pitch) {
         const uint64_t rows = outer_b ? a.C : a.J, cols = outer_b ? a.J : a.C, groups = !outer_a && a.groups ? a.groups : 1;
-        const hipError_t e =
-            copy_rows(a.b, outer_b ? a.b_c : a.b_j, a.b_group, groups, rows, cols, es, ws + q.b_at, q.b_pitch, s);
-        if (e != hipSuccess) return e;
+        cb = row_copy(a.b, outer_b ? a.b_c : a.b_j, a.b_group, groups, rows, cols, es, ws + q.b_at, q.b_pitch);
         a.b = ws + q.b_at;
         (outer_b ? a.b_c : a.b_j) = q.b_pitch;
         a.b_group = rows * q.b_pitch;
     }
+    const uint64_t copies = (uint64_t)ca.blocks + cb.blocks;
+    if (copies > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (copies && es == 1)
+        copy_rows_kernel<uint8_t><<<(uint32_t)copies, 256, 0, s>>>(ca, cb);
+    else if (copies)
+        copy_rows_kernel<uint16_t><<<(uint32_t)copies, 256, 0, s>>>(ca, cb);
     a.tiles_i = q.tiles_i;
     a.tiles_j = q.tiles_j;
     a.splits = q.splits;
