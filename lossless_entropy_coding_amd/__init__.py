@@ -5,6 +5,9 @@ only marshals arguments: every step of the path runs in the library's HIP
 kernels or its host codebook builders.  PyTorch provides device memory and
 streams.  There is no CPU fallback: if ``libec.so`` is missing the import of
 an entry point raises.
+
+The operators of feed-forward layers (``linear``, ``grouped_linear``,
+``layer_norm`` and their backward passes) are bound in ``ffn``.
 """
 
 from __future__ import annotations
