@@ -795,7 +795,7 @@ enum ShapeId { kHuge, kEven, kSmall, kFew };
 // What a plan's time is made of, measured on whole runs (us): a stage of one
 // workgroup alone on its CU, a stage per workgroup where every CU is full, and
 // what a workgroup costs besides its stages; bf16 and e4m3.  The full rates
-// are 1.07, 0.87 and 0.51 PFLOP/s in bf16.
+// are 1.25, 0.87 and 0.51 PFLOP/s in bf16.
 struct ShapeCost {
     uint32_t TI, TJ, per_cu;
     float alone[2], full[2], fixed;
