@@ -108,15 +108,14 @@ struct Factor {
         left -= (int64_t)step;
     }
 
-    // Load k of that stage, to the stage's place in LDS.  The compiler may make
-    // d with vector instructions, after which a memory instruction needs five
-    // wait states, and it does not count them for inline assembly: one here is
-    // the move to m0, four the s_nop.
+    // Load k of that stage, to the stage's place in LDS (in m0).  The compiler
+    // may make d with vector instructions, after which a memory instruction
+    // needs five wait states, and it does not count them for inline assembly.
     __device__ __forceinline__ void load(int k, uint32_t at, uint32_t wave) {
         const uint32_t q = (k * W + wave) % kInstr;
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at + q * 1024),
-                     "v"(off[k] | out), "s"(d)
-                     : "memory", "m0");
+        asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off[k] | out), "s"(d),
+                     "{m0}"(at + q * 1024)
+                     : "memory");
     }
 };
 
