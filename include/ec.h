@@ -520,8 +520,11 @@ int bf16_exp_decode(const uint8_t *d_in, uint64_t in_len, uint16_t *d_out, uint6
  * to the element's own alignment, are free; 16-byte aligned pointers with row
  * strides and row lengths that are multiples of 16 bytes are read in place,
  * any other factor of a product is first copied into the workspace (rows
- * padded to 16 bytes), unless a forward product has at most 32 rows (on
- * average by group), which reads rows at any address.  Sizes up to 2^31 - 1.
+ * padded to 16 bytes), and so is one whose row stride passes 8 to 64 MiB (by
+ * tile and direction).  Neither is a factor of a forward product of at most
+ * 32 rows (on average by group), which reads rows at any address.  Sizes up
+ * to 2^31 - 1; the backward products return EC_E_UNSUPPORTED for longer rows
+ * than they say.
  * ------------------------------------------------------------------------- */
 
 typedef enum ec_dtype {
@@ -613,6 +616,7 @@ int linear_forward(const ec_linear_args *a, hipStream_t stream);
  * dx[m, k] = act'(preact[m, k]) sum_n dy[m, n] w[n, k]
  * for bf16 dy, w; preact (bf16) is the input of the activation that made x,
  * required unless act is EC_ACT_NONE.  Reads d_dy, d_w, d_preact; writes d_dx.
+ * n up to 2^24 - 1024, k up to 2^25 - 2048.
  */
 int linear_grad_input(const ec_linear_args *a, hipStream_t stream);
 
@@ -620,7 +624,7 @@ int linear_grad_input(const ec_linear_args *a, hipStream_t stream);
  * dw[n, k] = sum_m dy[m, n] x[m, k]   (out_dtype EC_BF16 or EC_FP32)
  * db[n]    = sum_m dy[m, n]           (fp32)
  * over each group's rows, fixed order of summation.  Reads d_dy, d_x; writes
- * d_dw and d_db, whichever is given.
+ * d_dw and d_db, whichever is given.  With d_dw, n and k up to 2^25 - 2048.
  */
 int linear_grad_weight(const ec_linear_args *a, hipStream_t stream);
 

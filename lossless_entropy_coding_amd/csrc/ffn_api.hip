@@ -177,6 +177,7 @@ ColumnSumArgs column_sum(const ec_linear_args *a) {
 }
 
 int run_product(const ec_linear_args *a, const ProductArgs &p, hipStream_t stream) {
+    if (!product_fits(p)) return EC_E_UNSUPPORTED;
     const uint64_t need = product_workspace(p);
     if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;
     return hip_code(launch_product(p, a->d_workspace, stream));

@@ -65,6 +65,7 @@ struct ColumnSumArgs {                     // db
     uint32_t *status;
 };
 
+bool product_fits(const ProductArgs &a);            // whether some tile can address its rows
 uint64_t product_workspace(const ProductArgs &a);
 bool product_sums_columns(const ProductArgs &a);    // whether the product can write db as well
 hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s);

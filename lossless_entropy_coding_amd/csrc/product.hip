@@ -812,16 +812,21 @@ struct Plan {
     uint32_t row_tiles, waves;              // kFew
     uint64_t blocks;
     uint32_t a_pitch, b_pitch;              // elements; 0: read in place
+    bool none;                              // rows too long for every shape
     uint64_t a_at, b_at, partial_at, bytes; // workspace
 };
 
 uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 uint64_t round_up(uint64_t a, uint64_t b) { return ceil_div(a, b) * b; }
 
-bool readable(const void *p, uint64_t stride, uint64_t group, uint64_t cols, uint32_t es, bool outer) {
-    if (((uintptr_t)p | (stride * es) | (group * es)) & 15) return false;
-    if (!outer && (cols * es & 15)) return false;
-    return 256 * stride * es + 65536 < (1ull << 31); // a tile's offsets fit 31 bits
+bool aligned(const void *p, uint64_t stride, uint64_t group, uint64_t cols, uint32_t es, bool outer) {
+    return !((((uintptr_t)p | (stride * es) | (group * es)) & 15) || (!outer && (cols * es & 15)));
+}
+
+// Whether the offsets of a stage's rows fit 31 bits: T rows of a tile where
+// they are contiguous along the contraction, or the stage's rows of it.
+bool reachable(uint64_t T, uint64_t stride, uint32_t es, bool outer) {
+    return (outer ? kStageBytes / es : T) * stride * es + 65536 < (1ull << 31);
 }
 
 Plan make_plan(const ProductArgs &a) {
@@ -836,56 +841,74 @@ Plan make_plan(const ProductArgs &a) {
     const auto most_tiles = [&](uint64_t tile) {
         return ragged ? a.I / tile + (a.I < groups + 2 ? a.I : groups + 2) : ceil_div(a.I, tile);
     };
-    // Few rows a group, forward: one row by 16384 x 2048 weights takes 13.5 us
-    // so, 20 us in tiles with a split contraction and its join.
-    const uint64_t rows = ragged ? ceil_div(a.I, groups) : a.I;
-    if (a.op == EC_LINEAR_FORWARD && rows <= 32) {
+    const auto few = [&](uint32_t row_tiles) {          // reads rows at any address, of any length
         q.shape = kFew;
         q.tiles_j = (uint32_t)ceil_div(a.J, 16);
-        // 17 to 32 rows: one tile of 32 reads the weights once, but two of 16
-        // use twice as many CUs (17 rows: 16384 columns 24 against 32 us, 2048
-        // columns of 16384 e4m3 values 22 against 18).
-        q.row_tiles = rows > 16 && q.tiles_j >= kCUs ? 2 : 1;
+        q.row_tiles = row_tiles;
         q.tiles_i = (uint32_t)most_tiles(16 * q.row_tiles);
         // Waves that share a contraction: with 1024 tiles four are enough
         // (16.4 us; 16.2 with eight), with 128 eight are better (13.4, 16.1).
         q.waves = (ragged ? groups : q.tiles_i) * q.tiles_j >= 2 * kCUs ? 4 : 8;
-        q.blocks = (uint64_t)q.tiles_i * q.tiles_j;     // reads rows at any address
+        q.blocks = (uint64_t)q.tiles_i * q.tiles_j;
+    };
+    // Few rows a group, forward: one row by 16384 x 2048 weights takes 13.5 us
+    // so, 20 us in tiles with a split contraction and its join.  17 to 32 rows:
+    // one tile of 32 reads the weights once, but two of 16 use twice as many
+    // CUs (17 rows: 16384 columns 24 against 32 us, 2048 columns of 16384 e4m3
+    // values 22 against 18).
+    const uint64_t rows = ragged ? ceil_div(a.I, groups) : a.I;
+    if (a.op == EC_LINEAR_FORWARD && rows <= 32) {
+        few(rows > 16 && ceil_div(a.J, 16) >= kCUs ? 2 : 1);
         return q;
     }
-    uint64_t at = 0;
-    if (a.C) {
-        const uint64_t a_rows = outer_a ? a.C : a.I, a_cols = outer_a ? a.I : a.C;
-        const uint64_t b_rows = outer_b ? a.C : a.J, b_cols = outer_b ? a.J : a.C;
-        if (!readable(a.a, outer_a ? a.a_c : a.a_i, 0, a_cols, es, outer_a)) {
-            q.a_pitch = (uint32_t)round_up(a_cols, 16 / es);
-            at += round_up(a_rows * q.a_pitch * es, 256);
-        }
-        q.b_at = at;
-        if (!readable(a.b, outer_b ? a.b_c : a.b_j, outer_a ? 0 : a.b_group, b_cols, es, outer_b)) {
-            q.b_pitch = (uint32_t)round_up(b_cols, 16 / es);
-            at += round_up((outer_a ? 1 : groups) * b_rows * q.b_pitch * es, 256);
-        }
-    }
-    // The tiles and the number of splits with the least time.
+    // The tiles and the number of splits with the least time, of the shapes
+    // whose tiles reach their rows: where these lie, or else in a copy.
+    const uint64_t a_rows = outer_a ? a.C : a.I, a_cols = outer_a ? a.I : a.C, a_stride = outer_a ? a.a_c : a.a_i;
+    const uint64_t b_rows = outer_b ? a.C : a.J, b_cols = outer_b ? a.J : a.C, b_stride = outer_b ? a.b_c : a.b_j;
+    const uint64_t a_pitch = round_up(a_cols, 16 / es), b_pitch = round_up(b_cols, 16 / es);
+    const bool a_aligned = aligned(a.a, a_stride, 0, a_cols, es, outer_a);
+    const bool b_aligned = aligned(a.b, b_stride, outer_a ? 0 : a.b_group, b_cols, es, outer_b);
+    const uint64_t a_bytes = round_up(a_rows * a_pitch * es, 256);
+    const uint64_t b_bytes = round_up((outer_a ? 1 : groups) * b_rows * b_pitch * es, 256);
     const uint64_t stages = ceil_div((outer_a ? ceil_div(a.C, groups) : (uint64_t)a.C) * es, kStageBytes);
     float best = 0.0f;
     for (uint32_t id = kHuge; id <= kSmall; ++id) {
         const ShapeCost &c = kCost[id];
+        float copies = 0.0f;                            // what this shape has copied and another need not, at 4 TB/s
+        bool copy_a = false, copy_b = false;
+        if (a.C) {
+            copy_a = !a_aligned || !reachable(c.TI, a_stride, es, outer_a);
+            copy_b = !b_aligned || !reachable(c.TJ, b_stride, es, outer_b);
+            if ((copy_a && !reachable(c.TI, a_pitch, es, outer_a)) || (copy_b && !reachable(c.TJ, b_pitch, es, outer_b)))
+                continue;
+            copies = ((copy_a && a_aligned ? a_bytes : 0) + (copy_b && b_aligned ? b_bytes : 0)) * 0.5e-6f;
+        }
         const uint64_t ti = ragged ? a.I / c.TI + (groups + 1) / 2 : ceil_div(a.I, c.TI);
         const uint64_t tiles = ti * ceil_div(a.J, c.TJ) * (outer_a ? groups : 1);
         for (uint32_t n = 1; n == 1 || (!a.groups && n <= 32 && stages / n >= 8); n *= 2) {
             const uint64_t rounds = ceil_div(tiles * n, kCUs * c.per_cu), each = ceil_div(stages, n);
             const float alone = rounds * c.alone[es == 1], full = ceil_div(tiles * n, kCUs) * c.full[es == 1];
-            float t = (alone > full ? alone : full) * each + c.fixed * rounds;
+            float t = (alone > full ? alone : full) * each + c.fixed * rounds + copies;
             if (n > 1) t += 4.0f + (float)n * a.I * a.J * 1e-6f;      // the partial sums' bytes at 4 TB/s
             if (!best || t < best) {
                 best = t;
                 q.shape = id;
                 q.splits = n;
+                q.a_pitch = copy_a ? (uint32_t)a_pitch : 0;
+                q.b_pitch = copy_b ? (uint32_t)b_pitch : 0;
             }
         }
     }
+    if (!best) {                                        // rows of more than 32 MiB
+        if (a.op == EC_LINEAR_FORWARD)
+            few(2);
+        else
+            q.none = true;
+        return q;
+    }
+    uint64_t at = q.a_pitch ? a_bytes : 0;
+    q.b_at = at;
+    if (q.b_pitch) at += b_bytes;
     const uint32_t TI = kCost[q.shape].TI, TJ = kCost[q.shape].TJ;
     const uint64_t ti = most_tiles(TI);
     q.tiles_i = (uint32_t)ti;
@@ -944,6 +967,8 @@ bool product_sums_columns(const ProductArgs &a) {
     return a.op == EC_LINEAR_GRAD_WEIGHT && a.I && a.J && (a.groups || (a.C <= 1024 && make_plan(a).splits == 1));
 }
 
+bool product_fits(const ProductArgs &a) { return !a.I || !a.J || !make_plan(a).none; }
+
 uint64_t product_workspace(const ProductArgs &a) {
     if (!a.I || !a.J) return 0;
     return make_plan(a).bytes;
@@ -952,7 +977,7 @@ uint64_t product_workspace(const ProductArgs &a) {
 hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s) {
     if (!a.I || !a.J) return hipSuccess;
     const Plan q = make_plan(a);
-    if (q.blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (q.none || q.blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     const uint32_t es = a.dtype == EC_E4M3 ? 1 : 2;
     const bool outer_a = a.op == EC_LINEAR_GRAD_WEIGHT, outer_b = a.op != EC_LINEAR_FORWARD;
     char *ws = (char *)workspace;
