@@ -77,6 +77,13 @@ int check_grad_weight(const ec_linear_args *a) {
 
 int hip_code(hipError_t e) { return e == hipSuccess ? EC_OK : EC_E_HIP; }
 
+// A factor's row stride.  That of a single row may hold anything: the row's
+// length (whole 16-byte chunks) instead, past which a tile finds its end.
+uint64_t row_stride(uint64_t rows, uint64_t cols, uint64_t stride, uint32_t dtype) {
+    const uint64_t chunk = 16 / size_of(dtype);
+    return rows > 1 ? stride : (cols + chunk - 1) / chunk * chunk;
+}
+
 ProductArgs product(const ec_linear_args *a, uint32_t op) {
     ProductArgs p;
     memset(&p, 0, sizeof(p));
@@ -92,10 +99,10 @@ ProductArgs product(const ec_linear_args *a, uint32_t op) {
         p.J = (uint32_t)a->n;
         p.C = (uint32_t)a->k;
         p.a = a->d_x;
-        p.a_i = a->x_stride;
+        p.a_i = row_stride(a->m, a->k, a->x_stride, a->dtype);
         p.a_c = 1;
         p.b = a->d_w;
-        p.b_j = a->w_stride;
+        p.b_j = row_stride(a->n, a->k, a->w_stride, a->dtype);
         p.b_c = 1;
         p.b_group = a->w_group_stride;
         p.act = a->act;
@@ -116,11 +123,11 @@ ProductArgs product(const ec_linear_args *a, uint32_t op) {
         p.J = (uint32_t)a->k;
         p.C = (uint32_t)a->n;
         p.a = a->d_dy;
-        p.a_i = a->dy_stride;
+        p.a_i = row_stride(a->m, a->n, a->dy_stride, a->dtype);
         p.a_c = 1;
         p.b = a->d_w;
         p.b_j = 1;
-        p.b_c = a->w_stride;
+        p.b_c = row_stride(a->n, a->k, a->w_stride, a->dtype);
         p.b_group = a->w_group_stride;
         p.act = a->act;
         p.out_dtype = EC_BF16;
@@ -132,10 +139,10 @@ ProductArgs product(const ec_linear_args *a, uint32_t op) {
         p.C = (uint32_t)a->m;
         p.a = a->d_dy;
         p.a_i = 1;
-        p.a_c = a->dy_stride;
+        p.a_c = row_stride(a->m, a->n, a->dy_stride, a->dtype);
         p.b = a->d_x;
         p.b_j = 1;
-        p.b_c = a->x_stride;
+        p.b_c = row_stride(a->m, a->k, a->x_stride, a->dtype);
         p.out_dtype = a->out_dtype;
         p.out = a->d_dw;
         p.out_stride = a->dw_stride;
