@@ -105,7 +105,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float *sh) {
 template <bool F32, bool WHOLE, int BLOCK, int THREADS, int V>
 __global__ __launch_bounds__(BLOCK) void norm_kernel(NormArgs p) {
     constexpr int kRows = BLOCK / THREADS;                          // a workgroup's rows at a time
-    __shared__ float sh[16];
+    __shared__ float sh[32];
     const uint32_t t = threadIdx.x % THREADS;
     const float scale = p.out_scale ? *p.out_scale : 1.0f, cols = (float)p.cols;
     // weight and bias stay in registers over the rows, and the next row is
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(BLOCK) void norm_kernel(NormArgs p) {
     for (uint64_t first = (uint64_t)blockIdx.x * kRows; first < p.rows; first += step) {
         const uint64_t row = first + threadIdx.x / THREADS;
         const bool in = row < p.rows;
-        float x[V][8], s[1] = {0.0f};
+        float x[V][8], s[1] = {0.0f}, m[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < V; ++v) ahead[v].get(x[v]);
         if (first + step < p.rows) load(row + step);
@@ -142,19 +142,25 @@ __global__ __launch_bounds__(BLOCK) void norm_kernel(NormArgs p) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) s[0] += x[v][q];
         row_sum<THREADS>(s, sh);
-        const float mean = s[0] / cols;                             // a constant row's mean is its value
-        s[0] = 0.0f;
+        // The sum's rounding leaves `near` off by a part of itself, which a row
+        // far from zero would take for its spread: the mean of what is left is
+        // summed beside the squares and taken out of both.  A constant row's
+        // mean becomes its value, and its variance zero.
+        const float near = s[0] / cols;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const uint32_t left = left_of<WHOLE>(p.cols, 8 * (v * THREADS + t));
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                x[v][q] -= mean;
-                s[0] += q < (int)left ? x[v][q] * x[v][q] : 0.0f;
+                x[v][q] -= near;
+                m[0] += q < (int)left ? x[v][q] : 0.0f;
+                m[1] += q < (int)left ? x[v][q] * x[v][q] : 0.0f;
             }
         }
-        row_sum<THREADS>(s, sh);
-        const float rstd = 1.0f / sqrtf(s[0] / cols + p.eps);
+        row_sum<THREADS>(m, sh);
+        const float off = m[0] / cols, mean = near + off;
+        const float var = __builtin_fmaf(-off, off, m[1] / cols);
+        const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + p.eps);
         if (!in) continue;
         if (t == 0) {
             if (p.mean) p.mean[row] = mean;
@@ -170,7 +176,7 @@ __global__ __launch_bounds__(BLOCK) void norm_kernel(NormArgs p) {
                 load_param<WHOLE>(p.bias, p.w_dtype, c, left, 0.0f, b[0]);
             }
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[v][q] = (x[v][q] * rstd * w[k][q] + b[k][q]) * scale;
+            for (int q = 0; q < 8; ++q) x[v][q] = ((x[v][q] - off) * rstd * w[k][q] + b[k][q]) * scale;
             store8(p.y, p.out_dtype, row * p.y_stride + c, left, x[v]);
         }
     }
