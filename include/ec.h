@@ -608,7 +608,8 @@ uint64_t linear_workspace_bytes(const ec_linear_args *a, uint32_t op);
  * preact  = bf16(z)                                    (when d_preact)
  * y       = out_dtype(act(z) + residual[m, n])         (EC_E4M3: times *d_out_scale, saturating, ties to even)
  * Products and sums in fp32; one rounding, at the store.  Asynchronous on
- * `stream`; allocates nothing.
+ * `stream`; allocates nothing.  y may be the residual itself (the same pointer
+ * and stride); outputs overlap nothing else that is read.
  */
 int linear_forward(const ec_linear_args *a, hipStream_t stream);
 
@@ -616,7 +617,8 @@ int linear_forward(const ec_linear_args *a, hipStream_t stream);
  * dx[m, k] = act'(preact[m, k]) sum_n dy[m, n] w[n, k]
  * for bf16 dy, w; preact (bf16) is the input of the activation that made x,
  * required unless act is EC_ACT_NONE.  Reads d_dy, d_w, d_preact; writes d_dx.
- * n up to 2^24 - 1024, k up to 2^25 - 2048.
+ * dx may be the preact itself (the same pointer and stride).  n up to 2^24 -
+ * 1024, k up to 2^25 - 2048.
  */
 int linear_grad_input(const ec_linear_args *a, hipStream_t stream);
 
@@ -634,7 +636,8 @@ int linear_grad_weight(const ec_linear_args *a, hipStream_t stream);
  *   y = (x - mean) rstd weight + bias     in out_dtype (EC_E4M3: times *d_out_scale, saturating)
  * weight and bias are [cols] of type w_dtype (EC_BF16 or EC_FP32), each or
  * both NULL for 1 and 0.  d_mean and d_rstd (fp32 [rows]) may be NULL.
- * Statistics in fp32 from the centred values.  cols up to 65536.
+ * Statistics in fp32 from the centred values.  cols up to 65536.  y may be x
+ * itself (the same pointer, type and stride).
  */
 int layer_norm_forward(const void *d_x, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_stride,
                        const void *d_weight, const void *d_bias, uint32_t w_dtype, float eps, void *d_y,
@@ -649,7 +652,9 @@ uint64_t layer_norm_grad_workspace_bytes(uint64_t rows, uint64_t cols);
  *   dx = rstd (t - mean_c(t) - h mean_c(t h)) + dres
  *   dweight = sum_rows dy h,  dbias = sum_rows dy      (fp32, fixed order)
  * dy, x, dres, dx are of type dtype (EC_BF16 or EC_FP32); dres may be NULL,
- * and so may d_dx, or d_dweight and d_dbias (each).
+ * and so may d_dx, or d_dweight and d_dbias (each).  dx may be dy, x or dres
+ * itself (the same pointer and stride); beyond 8192 columns not dy or x, where
+ * any overlap with them is refused.
  */
 int layer_norm_grad(const void *d_dy, uint64_t dy_stride, const void *d_x, uint64_t x_stride, uint32_t dtype,
                     uint64_t rows, uint64_t cols, const float *d_mean, const float *d_rstd,

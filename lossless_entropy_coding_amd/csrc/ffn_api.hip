@@ -75,6 +75,18 @@ int check_grad_weight(const ec_linear_args *a) {
     return ((uintptr_t)a->d_db & 3) == 0 ? EC_OK : EC_E_INVAL;
 }
 
+// Whether two [rows, cols] tensors share memory; of different strides, whether
+// what they span does.
+bool overlap(const void *p, uint64_t p_stride, const void *q, uint64_t q_stride, uint64_t rows, uint64_t cols,
+             uint64_t size) {
+    if (!rows || !cols) return false;
+    const uint64_t a = (uint64_t)(uintptr_t)p, b = (uint64_t)(uintptr_t)q, row = cols * size;
+    if (a + (rows - 1) * p_stride * size + row <= b || b + (rows - 1) * q_stride * size + row <= a) return false;
+    if (rows == 1 || p_stride != q_stride) return true;
+    const uint64_t step = p_stride * size, apart = (a < b ? b - a : a - b) % step;
+    return apart < row || apart + row > step;       // not side by side
+}
+
 int hip_code(hipError_t e) { return e == hipSuccess ? EC_OK : EC_E_HIP; }
 
 // A factor's row stride.  That of a single row may hold anything: the row's
@@ -280,6 +292,11 @@ int layer_norm_grad(const void *d_dy, uint64_t dy_stride, const void *d_x, uint6
     if (rows && (!d_mean || !d_rstd)) return EC_E_INVAL;
     if (d_dres && !tensor_ok(d_dres, dtype, rows, cols, dres_stride)) return EC_E_INVAL;
     if (d_dx && !tensor_ok(d_dx, dtype, rows, cols, dx_stride)) return EC_E_INVAL;
+    // workgroups that share a row read all of it, in no order with its dx
+    const uint64_t size = size_of(dtype);
+    if (d_dx && norm_grad_slices(cols) > 1 &&
+        (overlap(d_dx, dx_stride, d_x, x_stride, rows, cols, size) || overlap(d_dx, dx_stride, d_dy, dy_stride, rows, cols, size)))
+        return EC_E_INVAL;
     if (((uintptr_t)d_mean | (uintptr_t)d_rstd | (uintptr_t)d_dweight | (uintptr_t)d_dbias) & 3) return EC_E_INVAL;
     if ((d_dweight || d_dbias) && (!d_workspace || ((uintptr_t)d_workspace & 15) ||
                                    workspace_bytes < layer_norm_grad_workspace_bytes(rows, cols)))

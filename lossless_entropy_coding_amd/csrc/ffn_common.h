@@ -97,6 +97,7 @@ struct NormGradArgs {
 
 hipError_t launch_norm(const NormArgs &a, hipStream_t s);
 uint32_t norm_grad_parts(uint64_t rows, uint64_t cols);
+uint32_t norm_grad_slices(uint64_t cols);              // workgroups that share a row
 hipError_t launch_norm_grad(const NormGradArgs &a, hipStream_t s);
 
 // ---------------------------------------------------------------- conversions

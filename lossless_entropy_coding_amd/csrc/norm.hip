@@ -186,7 +186,7 @@ __global__ __launch_bounds__(BLOCK) void norm_kernel(NormArgs p) {
 // dbias for its columns in registers; they are joined over its rows in LDS
 // and written once.  Rows wider than THREADS * V * 8 are cut into slices
 // (blockIdx.y): each slice's workgroup sums over the whole row, but writes dx
-// and the sums of its own columns only.
+// and the sums of its own columns only, so dx may not lie over x or dy there.
 template <bool F32, bool WHOLE, int THREADS, int V>
 __global__ __launch_bounds__(512) void norm_grad_kernel(NormGradArgs p) {
     constexpr int kRows = 512 / THREADS, kSlice = THREADS * V * 8;
@@ -398,6 +398,9 @@ uint32_t norm_grad_parts(uint64_t rows, uint64_t cols) {
     const uint64_t at_once = 512 / grad_threads(cols), need = (rows + at_once - 1) / at_once;
     return (uint32_t)(need < 1 ? 1 : need < 512 ? need : 512);
 }
+
+// Only the widest kernel, of two chunks in 512 threads, cuts rows.
+uint32_t norm_grad_slices(uint64_t cols) { return (uint32_t)((cols + 8191) / 8192); }
 
 hipError_t launch_norm_grad(const NormGradArgs &a, hipStream_t s) {
     if (a.dx || a.partial) a.dtype == EC_FP32 ? pick_norm_grad<true>(a, s) : pick_norm_grad<false>(a, s);

@@ -414,7 +414,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, residual_grad=None, n
 
     Returns (dx, dweight, dbias), None where not needed.  residual_grad (x's
     type) is added to dx: the gradient that reaches x past the norm.  dweight
-    and dbias are float32 [cols], summed in a fixed order."""
+    and dbias are float32 [cols], summed in a fixed order.  dx may be dy, x or
+    residual_grad itself, beyond 8192 columns only the last."""
     ec = _ec()
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         _error("x must be a 2-D CUDA tensor")
