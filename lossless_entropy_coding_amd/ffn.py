@@ -124,15 +124,18 @@ def _placed(fn):
     and workspaces come from that stream's memory, so none is in use by work
     queued elsewhere.  The first tensor's device becomes the current one."""
 
+    first = fn.__code__.co_varnames[0]      # may be given by its name, like any other
+
     @functools.wraps(fn)
-    def call(t, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         if stream is not None:
             with torch.cuda.stream(stream):
-                return call(t, *args, **kw)
+                return call(*args, **kw)
+        t = args[0] if args else kw.get(first)
         if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
             with torch.cuda.device(t.device):
-                return fn(t, *args, **kw)
-        return fn(t, *args, **kw)
+                return fn(*args, **kw)
+        return fn(*args, **kw)
 
     return call
 

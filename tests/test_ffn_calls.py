@@ -1,0 +1,62 @@
+"""How the feed-forward operators may be called: arguments by name, streams,
+wrong kinds of objects, tensors that require gradients."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def ec():
+    import os
+    import lossless_entropy_coding_amd as ec
+    if not os.path.exists(ec.LIB_PATH):
+        import __graft_entry__
+        __graft_entry__.build()
+    ec.lib()
+    return ec
+
+
+def _inputs(device):
+    g = torch.Generator().manual_seed(2)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=g).bfloat16().to(device)
+
+    return dict(x=randn(5, 16), w=randn(8, 16), dy=randn(5, 8), dyn=randn(5, 16), we=randn(2, 8, 16),
+                off=torch.tensor([0, 2, 5], dtype=torch.int32, device=device),
+                mean=torch.zeros(5, device=device), rstd=torch.ones(5, device=device))
+
+
+def _calls(ec, t):
+    """(by position, by name) for each of the six."""
+    return [
+        (lambda: ec.linear(t["x"], t["w"]), lambda: ec.linear(w=t["w"], x=t["x"])),
+        (lambda: ec.grouped_linear(t["x"], t["we"], t["off"]),
+         lambda: ec.grouped_linear(offsets=t["off"], x=t["x"], w=t["we"])),
+        (lambda: ec.linear_backward(t["dy"], t["x"], t["w"]), lambda: ec.linear_backward(x=t["x"], w=t["w"], dy=t["dy"])),
+        (lambda: ec.grouped_linear_backward(t["dy"], t["x"], t["we"], t["off"]),
+         lambda: ec.grouped_linear_backward(dy=t["dy"], x=t["x"], w=t["we"], offsets=t["off"])),
+        (lambda: ec.layer_norm(t["x"]), lambda: ec.layer_norm(x=t["x"], eps=1e-5)),
+        (lambda: ec.layer_norm_backward(t["dyn"], t["x"], t["mean"], t["rstd"]),
+         lambda: ec.layer_norm_backward(dy=t["dyn"], x=t["x"], mean=t["mean"], rstd=t["rstd"])),
+    ]
+
+
+def test_names_reach_the_checks(ec):
+    """On host tensors every call is refused by the operator's own checks, however its arguments are given."""
+    for calls in _calls(ec, _inputs("cpu")):
+        for call in calls:
+            with pytest.raises(ec.ECError):
+                call()
+    for f in (ec.linear, ec.layer_norm, ec.linear_backward):
+        with pytest.raises(TypeError):
+            f()
+
+
+@pytest.mark.gpu
+def test_names_give_the_same(ec):
+    for by_position, by_name in _calls(ec, _inputs("cuda")):
+        a, b = by_position(), by_name()
+        a, b = (v if isinstance(v, tuple) else (v,) for v in (a, b))
+        assert len(a) == len(b) and all(torch.equal(p, q) for p, q in zip(a, b))
