@@ -122,16 +122,19 @@ def _empty(shape, dtype, device):
 def _placed(fn):
     """``stream=s`` runs the call as under ``torch.cuda.stream(s)``: outputs
     and workspaces come from that stream's memory, so none is in use by work
-    queued elsewhere.  The first tensor's device becomes the current one."""
+    queued elsewhere.  The first tensor's device becomes the current one; a
+    stream of another is refused."""
 
     first = fn.__code__.co_varnames[0]      # may be given by its name, like any other
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
+        t = args[0] if args else kw.get(first)
         if stream is not None:
+            if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
+                _error("stream is on %s, %s on %s" % (stream.device, first, t.device))
             with torch.cuda.stream(stream):
                 return call(*args, **kw)
-        t = args[0] if args else kw.get(first)
         if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
             with torch.cuda.device(t.device):
                 return fn(*args, **kw)

@@ -60,3 +60,23 @@ def test_names_give_the_same(ec):
         a, b = by_position(), by_name()
         a, b = (v if isinstance(v, tuple) else (v,) for v in (a, b))
         assert len(a) == len(b) and all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.gpu
+def test_stream_of_another_device_is_refused(ec):
+    """Only what the binding reads of a stream: there may be no second device here to make one on."""
+    class Elsewhere:
+        device = torch.device("cuda", torch.cuda.current_device() + 1)
+        cuda_stream = 0
+
+    t = _inputs("cuda")
+    for call in [lambda s: ec.linear(t["x"], t["w"], stream=s), lambda s: ec.layer_norm(x=t["x"], stream=s),
+                 lambda s: ec.grouped_linear(t["x"], t["we"], t["off"], stream=s),
+                 lambda s: ec.linear_backward(t["dy"], t["x"], t["w"], stream=s)]:
+        with pytest.raises(ec.ECError, match="stream"):
+            call(Elsewhere)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = ec.linear(x=t["x"], w=t["w"], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, ec.linear(t["x"], t["w"]))
