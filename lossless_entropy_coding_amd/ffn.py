@@ -179,10 +179,18 @@ def _weights(w, name: str, offsets, dtypes):
     return groups, n, k, stride, (w.stride(0) if groups > 1 else 0)
 
 
+def _given(t, name: str, dtype) -> None:
+    """A tensor to write to that the caller has given, and the type asked for with it (or None)."""
+    if not isinstance(t, torch.Tensor):
+        _error("%s must be a tensor, not %s" % (name, type(t).__name__))
+    if dtype is not None and t.dtype != dtype:
+        _error("%s is %s, %s_dtype %s" % (name, t.dtype, name, dtype))
+
+
 def _status(status, device):
     if status is None:
         return None
-    if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
+    if not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.device != device or status.numel() < 1:
         _error("status must be an int32 tensor on %s" % device)
     return status.data_ptr()
 
@@ -224,8 +232,7 @@ def _forward(x, w, offsets, bias, act, residual, x_scale, w_scale, out_scale, ou
             _error("out_dtype must be bfloat16, float32, float8_e4m3fn or uint8 (e4m3 bytes), not %s" % out_dtype)
         out, a.y_stride = _empty((m, n), out_dtype, dev), n
     else:
-        if out_dtype is not None and out.dtype != out_dtype:
-            _error("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        _given(out, "out", out_dtype)
         a.y_stride = _matrix(out, "out", m, n, _DTYPES, dev)
     a.y, a.out_dtype = out.data_ptr(), _DTYPES[out.dtype]
     if out_scale is not None:
@@ -310,8 +317,8 @@ def _backward(dy, x, w, offsets, preact, act, need_dx, need_dw, need_db, dw_dtyp
             a.x_stride, a.x = _matrix(x, "x", m, k, bf, dev), x.data_ptr()
             if dw is None:
                 dw = _empty(per + (n, k), dw_dtype if dw_dtype is not None else torch.bfloat16, dev)
-            elif dw_dtype is not None and dw.dtype != dw_dtype:
-                _error("dw is %s, dw_dtype %s" % (dw.dtype, dw_dtype))
+            else:
+                _given(dw, "dw", dw_dtype)
             if tuple(dw.shape) != per + (n, k) or dw.device != dev:
                 _error("dw must be %s on %s" % (list(per + (n, k)), dev))
             if dw.dtype not in (torch.bfloat16, torch.float32):
@@ -394,8 +401,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, out_dtype=None, 
             _error("out_dtype must be bfloat16, float32, float8_e4m3fn or uint8 (e4m3 bytes), not %s" % out_dtype)
         out, ys = _empty((rows, cols), out_dtype, dev), cols
     else:
-        if out_dtype is not None and out.dtype != out_dtype:
-            _error("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        _given(out, "out", out_dtype)
         ys = _matrix(out, "out", rows, cols, _DTYPES, dev)
     if out_scale is not None:
         if _DTYPES[out.dtype] != _E4M3:

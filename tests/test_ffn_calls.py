@@ -80,3 +80,25 @@ def test_stream_of_another_device_is_refused(ec):
     y = ec.linear(x=t["x"], w=t["w"], stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(y, ec.linear(t["x"], t["w"]))
+
+
+@pytest.mark.gpu
+def test_objects_that_are_no_tensors_are_refused(ec):
+    t = _inputs("cuda")
+    dev = [1.0]
+    bf = torch.bfloat16
+    for call in [lambda: ec.linear(t["x"], t["w"], out=dev, out_dtype=bf), lambda: ec.linear(t["x"], t["w"], out=dev),
+                 lambda: ec.linear(t["x"], t["w"], dev), lambda: ec.linear(t["x"], t["w"], residual=dev),
+                 lambda: ec.linear(t["x"], t["w"], preact=dev), lambda: ec.linear(t["x"], t["w"], x_scale=2.0),
+                 lambda: ec.grouped_linear(t["x"], t["we"], t["off"], status=0),
+                 lambda: ec.grouped_linear(t["x"], t["we"], [0, 2, 5]),
+                 lambda: ec.linear_backward(t["dy"], t["x"], t["w"], dw=dev),
+                 lambda: ec.linear_backward(t["dy"], t["x"], t["w"], dw=dev, dw_dtype=bf),
+                 lambda: ec.linear_backward(t["dy"], t["x"], t["w"], db=dev), lambda: ec.linear_backward(t["dy"], dev, t["w"]),
+                 lambda: ec.linear_backward(t["dy"], t["x"], t["w"], dx=dev),
+                 lambda: ec.linear_backward(t["dy"], t["x"], t["w"], preact=dev, act="gelu"),
+                 lambda: ec.layer_norm(t["x"], out=dev, out_dtype=bf), lambda: ec.layer_norm(t["x"], out=dev),
+                 lambda: ec.layer_norm(t["x"], mean=dev, rstd=dev), lambda: ec.layer_norm(t["x"], weight=1.0),
+                 lambda: ec.layer_norm_backward(t["dyn"], t["x"], t["mean"], 1.0)]:
+        with pytest.raises(ec.ECError):
+            call()
