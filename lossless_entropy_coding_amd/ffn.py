@@ -10,12 +10,17 @@ Tensors are 2-D (or have their leading dimensions flattened by the caller),
 rows may be strided, a row's elements are contiguous.  An e4m3 tensor is
 ``torch.float8_e4m3fn``; ``uint8`` is read as e4m3 bytes, so that what
 ``decode`` returns goes straight into a product.
+
+Autograd does not see these calls: gradients come from the backward functions
+here, called by the program.  A forward call warns where torch is recording
+and a tensor requires its gradient, since the result will not.
 """
 
 from __future__ import annotations
 
 import ctypes
 import functools
+import warnings
 
 import torch
 
@@ -143,6 +148,16 @@ def _placed(fn):
     return call
 
 
+def _warn_unrecorded(level: int, *tensors):
+    """`level`: frames between the caller's and this one."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                warnings.warn("autograd does not record this call: its result requires no gradient (use the backward "
+                              "functions, and torch.no_grad() here)", stacklevel=level + 2)
+                return
+
+
 def _call(name: str, args: _LinearArgs, op: int, device):
     ec = _ec()
     L = ec.lib()
@@ -246,6 +261,7 @@ def _forward(x, w, offsets, bias, act, residual, x_scale, w_scale, out_scale, ou
         else:
             a.preact_stride = _matrix(preact, "preact", m, n, (torch.bfloat16,), dev)
         a.preact = preact.data_ptr()
+    _warn_unrecorded(3, x, w, bias, residual)
     _call("linear_forward", a, _FORWARD, dev)
     return out if preact is None else (out, preact)
 
@@ -412,6 +428,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, out_dtype=None, 
     else:
         for t, name in ((mean, "mean"), (rstd, "rstd")):
             _vector(t, name, ((rows,),), (torch.float32,), dev)
+    _warn_unrecorded(2, x, weight, bias)
     ec._check(ec.lib().layer_norm_forward(x.data_ptr(), _DTYPES[x.dtype], rows, cols, xs, _ptr(weight), _ptr(bias),
                                           w_dtype, float(eps), out.data_ptr(), _DTYPES[out.dtype], ys,
                                           _ptr(out_scale), mean.data_ptr(), rstd.data_ptr(), ec._stream(None)),

@@ -102,3 +102,25 @@ def test_objects_that_are_no_tensors_are_refused(ec):
                  lambda: ec.layer_norm_backward(t["dyn"], t["x"], t["mean"], 1.0)]:
         with pytest.raises(ec.ECError):
             call()
+
+
+@pytest.mark.gpu
+def test_unrecorded_gradients_are_warned_of(ec):
+    """Where torch records and a tensor requires its gradient; the values are the same, and silent otherwise."""
+    import warnings
+    t = _inputs("cuda")
+    bias, res, norm = torch.ones(8, device="cuda"), torch.ones(5, 8, device="cuda").bfloat16(), torch.ones(16, device="cuda")
+    calls = [lambda g: ec.linear(g(t["x"]), t["w"]), lambda g: ec.linear(x=t["x"], w=g(t["w"])),
+             lambda g: ec.linear(t["x"], t["w"], g(bias)), lambda g: ec.linear(t["x"], t["w"], residual=g(res)),
+             lambda g: ec.grouped_linear(t["x"], g(t["we"]), t["off"]), lambda g: ec.layer_norm(g(t["x"]))[0],
+             lambda g: ec.layer_norm(t["x"], g(norm))[0]]
+    for call in calls:
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            want = call(lambda v: v)
+            with torch.no_grad():
+                assert torch.equal(call(lambda v: v.clone().requires_grad_()), want)
+        with pytest.warns(UserWarning, match="autograd does not record") as seen:
+            got = call(lambda v: v.clone().requires_grad_())
+        assert torch.equal(got, want) and not got.requires_grad
+        assert len(seen) == 1 and seen[0].filename == __file__
