@@ -234,7 +234,8 @@ int linear_grad_weight(const ec_linear_args *a, hipStream_t stream) {
         if (both) p.db = a->d_db;
         if ((rc = run_product(a, p, stream)) || both) return rc;
     }
-    if (!a->d_db) return EC_OK;
+    if (!a->d_db)       // neither, as where n is 0
+        return a->d_dw ? EC_OK : hip_code(launch_check_offsets(a->d_offsets, a->groups, (uint32_t)a->m, a->d_status, stream));
     const ColumnSumArgs c = column_sum(a);
     const uint64_t need = column_sum_workspace(c);
     if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;

@@ -69,6 +69,7 @@ bool product_fits(const ProductArgs &a);            // whether some tile can add
 uint64_t product_workspace(const ProductArgs &a);
 bool product_sums_columns(const ProductArgs &a);    // whether the product can write db as well
 hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s);
+hipError_t launch_check_offsets(const int32_t *offsets, uint32_t groups, uint32_t m, uint32_t *status, hipStream_t s);
 uint64_t column_sum_workspace(const ColumnSumArgs &a);
 hipError_t launch_column_sum(const ColumnSumArgs &a, float *workspace, hipStream_t s);
 

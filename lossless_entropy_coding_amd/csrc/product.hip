@@ -786,6 +786,12 @@ __global__ __launch_bounds__(256) void column_join_kernel(const float *in, float
     db[c] = s;
 }
 
+// For a grouped product that has nothing to compute.
+__global__ __launch_bounds__(64) void check_offsets_kernel(const int32_t *offsets, uint32_t groups, uint32_t m,
+                                                           uint32_t *status) {
+    check_offsets(offsets, groups, m, status);
+}
+
 // ---------------------------------------------------------------------- plan
 
 using Huge = Shape<256, 256, 2, 4, 4, 1>;
@@ -961,6 +967,12 @@ RowCopy row_copy(const void *p, uint64_t stride, uint64_t group_stride, uint64_t
 
 }  // namespace
 
+hipError_t launch_check_offsets(const int32_t *offsets, uint32_t groups, uint32_t m, uint32_t *status, hipStream_t s) {
+    if (!groups || !status) return hipSuccess;
+    check_offsets_kernel<<<1, 64, 0, s>>>(offsets, groups, m, status);
+    return hipGetLastError();
+}
+
 bool product_sums_columns(const ProductArgs &a) {
     // The second launch and its join cost 8 - 10 us, the sums a tenth of the
     // product: up to 1024 rows that is less (see product_kernel).
@@ -975,7 +987,8 @@ uint64_t product_workspace(const ProductArgs &a) {
 }
 
 hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s) {
-    if (!a.I || !a.J) return hipSuccess;
+    if (!a.I || !a.J)
+        return launch_check_offsets(a.offsets, a.groups, a.op == EC_LINEAR_GRAD_WEIGHT ? a.C : a.I, a.status, s);
     const Plan q = make_plan(a);
     if (q.none || q.blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     const uint32_t es = a.dtype == EC_E4M3 ? 1 : 2;
@@ -1031,7 +1044,7 @@ uint64_t column_sum_workspace(const ColumnSumArgs &a) {
 }
 
 hipError_t launch_column_sum(const ColumnSumArgs &a, float *workspace, hipStream_t s) {
-    if (!a.n) return hipSuccess;
+    if (!a.n) return launch_check_offsets(a.offsets, a.groups, a.m, a.status, s);
     const uint32_t parts = column_parts(a), groups = a.groups ? a.groups : 1;
     const uint64_t n = (uint64_t)groups * a.n;
     column_sum_kernel<<<dim3((uint32_t)ceil_div(a.n, kSumCols), groups, parts), 256, 0, s>>>(a, parts > 1 ? workspace : a.db,
