@@ -860,11 +860,17 @@ Plan make_plan(const ProductArgs &a) {
     // Few rows a group, forward: one row by 16384 x 2048 weights takes 13.5 us
     // so, 20 us in tiles with a split contraction and its join.  17 to 32 rows:
     // one tile of 32 reads the weights once, but two of 16 use twice as many
-    // CUs (17 rows: 16384 columns 24 against 32 us, 2048 columns of 16384 e4m3
-    // values 22 against 18).
+    // CUs, so that the tiles of 16 columns must be enough for them all (17 rows:
+    // 16384 columns 24 against 32 us, 2048 columns of 16384 e4m3 values 22
+    // against 18), twice over by group, where rows are uneven (20 rows by 1024 x
+    // 2048 a group, 32 groups: 50 us against 64, e4m3 22 against 38; uneven 61
+    // against 58, e4m3 30 against 34; four uneven groups 13.7 against 12.3).
+    // The average decides, since the host does not know the offsets: 1024 rows
+    // of which 962 are in one of 32 groups take 90 us so and 45 in tiles.
     const uint64_t rows = ragged ? ceil_div(a.I, groups) : a.I;
     if (a.op == EC_LINEAR_FORWARD && rows <= 32) {
-        few(rows > 16 && ceil_div(a.J, 16) >= kCUs ? 2 : 1);
+        const bool fill = ceil_div(a.J, 16) * groups >= (ragged ? 2 : 1) * kCUs;
+        few(rows > 16 && fill ? 2 : 1);
         return q;
     }
     // The tiles and the number of splits with the least time, of the shapes
