@@ -97,10 +97,12 @@ struct Factor {
     // Makes the next stage the one to load; `rest` is what remains of the
     // contraction, in bytes of a row (not OUTER): chunks past it read as zero.
     __device__ __forceinline__ void next(uint32_t rest, uint32_t lane) {
-        const int64_t n = left < 0 ? 0 : left > 0x7FFFFFFF ? 0x7FFFFFFF : left;
+        // by halves: the scalar unit does not compare 64 bits with a sign
+        const int32_t high = (int32_t)(left >> 32);
+        const uint32_t low = (uint32_t)left, n = high < 0 ? 0 : high > 0 || low > 0x7FFFFFFFu ? 0x7FFFFFFFu : low;
         d[0] = __builtin_amdgcn_readfirstlane((int)base);
         d[1] = __builtin_amdgcn_readfirstlane((int)(base >> 32) & 0xFFFF);
-        d[2] = __builtin_amdgcn_readfirstlane(rest ? (int)n : 0);
+        d[2] = __builtin_amdgcn_readfirstlane((int)(rest ? n : 0));
         d[3] = 0x00027000;
         out = 0;
         if constexpr (!OUTER) out = ((lane & 3) ^ ((lane >> 4) & 3)) * 16 < rest ? 0 : kOutside;
