@@ -547,7 +547,7 @@ typedef enum ec_act {
  * y [m, n].  Zero-initialise, then fill in what a function names; pointers it
  * does not name may be NULL.
  *
- * Grouped (groups > 0): group e's rows are offsets[e] .. offsets[e + 1) - 1
+ * Grouped (groups > 0): group e's rows are offsets[e] .. offsets[e + 1] - 1
  * of the m rows (device int32[groups + 1], never decreasing, within [0, m];
  * read on the device, never by the host), and it has its own w, bias and
  * w_scale: w [groups, n, k], bias [groups, n], w_scale [groups, w_scales].

@@ -8,9 +8,9 @@ namespace {
 // neighbouring values each (chunk v of thread t starts at column
 // 8 (v THREADS + t)), so x is read once and the variance is that of the
 // centred values.  Both passes are bound by the bytes they move: at 8192 x
-// 2048 in bf16 the forward pass takes 18.8 us (3.6 TB/s), the backward pass
-// 35.8 us (3.8 TB/s) and 4.2 us for the sums of its partial rows; a copy
-// reaches 4.8 TB/s.  One row of 2048 takes 2.6 us, a launch.
+// 2048 in bf16 the forward pass takes 19.0 us (3.5 TB/s), the backward pass
+// 36.3 us (3.7 TB/s) and 4.5 us for the sums of its partial rows; a copy
+// reaches 4.8 TB/s.  One row of 2048 takes 2.7 us, a launch.
 //
 // WHOLE: the columns are a multiple of eight, so a chunk is whole or empty.
 template <bool WHOLE>

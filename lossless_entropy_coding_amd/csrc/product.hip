@@ -25,10 +25,12 @@ typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 // power limit, which brings the clock under full load from 2.4 to 1.6 - 2.0
 // GHz (the same product of zeros runs 1.25 times as fast).  Eight waves of
 // 128 x 64 keep two waves a SIMD; four of 128 x 128 need all registers and
-// spill.  4096 x 16384 x 2048 bf16 with GELU and e4m3 output: 298 us (0.92
-// PFLOP/s); 4096 x 2048 x 16384 e4m3: 230 us with the join (1.2); backward of
-// 2048 x 16384 x 2048: 290 us (0.95).  Asking for lines ahead of their stage, or loading two stages at a
-// time (whole 128-byte lines), was slower where the weights come from HBM.
+// spill.  4096 x 16384 x 2048 bf16 with GELU and e4m3 output: 306 us (0.90
+// PFLOP/s; 300 to 315 by card); 4096 x 2048 x 16384 e4m3: 224 us with the join
+// (1.2); backward of 2048 x 16384 x 2048: 288 us (0.95).  One workgroup a CU
+// leaves its first loads and its epilogue exposed: 30% of the waves' time is
+// waiting.  Asking for lines ahead of their stage, or loading two stages at
+// a time (whole 128-byte lines), was slower where the weights come from HBM.
 template <int TI_, int TJ_, int WI_, int WJ_, int S_, int PER_CU_>
 struct Shape {
     static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, S = S_;
@@ -163,9 +165,10 @@ struct Multiply {
         if constexpr (E4M3) {
             // e4m3 values are exact in bf16, and the products of bf16 are added in
             // 32 bits.  The e4m3 instructions are not used: they cut the products
-            // they add to a few bits below the largest (measured: sums of 16 off
-            // by up to 2^-14 of the sum of magnitudes, against 2^-26 here), where
-            // sums are to be held in 32 bits.
+            // they add to a few bits below the largest (measured: sums of 16
+            // products of random bytes off by up to 2^-11.2 of the sum of
+            // magnitudes, against 2^-22.3 here), where sums are to be held in 32
+            // bits.
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 between(s);
@@ -243,7 +246,7 @@ __device__ __forceinline__ void finish_tiles(const ProductArgs &p, f32x16 (&acc)
     // The residual, or the activation's input, of all rows is asked for at
     // once, since every turn of 32 rows would wait for HBM anew (1023 x 2050:
     // 26.1 -> 23.9 us); the forward pass's large tiles have no registers left
-    // for that (320 us as it is, 338 with them spilled).
+    // for that (spilled, 4096 x 16384 x 2048 takes 6% longer).
     constexpr bool kSide = OP == EC_LINEAR_FORWARD || (OP == EC_LINEAR_GRAD_INPUT && ACT != EC_ACT_NONE);
     const uint16_t *const from = OP == EC_LINEAR_FORWARD ? p.residual : p.preact;
     const uint64_t stride = OP == EC_LINEAR_FORWARD ? p.residual_stride : p.preact_stride;
@@ -569,7 +572,7 @@ __global__ __launch_bounds__(T::THREADS) void join_kernel(ProductArgs p) {
 // B, and of its rows of A, at a time, 64 bytes of a row in a wave's load, and
 // the waves' sums are joined in LDS in the waves' order.  One row by 16384 x
 // 2048 bf16 weights: 13.6 us (4.9 TB/s); 64 rows over 32 experts of 1024 x
-// 2048: 26.7 us (5.0 TB/s); 17 rows by 2048 x 16384 e4m3 weights: 18.4 us, the
+// 2048: 26.8 us (5.0 TB/s); 17 rows by 2048 x 16384 e4m3 weights: 18.3 us, the
 // latency of 256 workgroups' loads.
 template <int RT, int W>
 struct Few {

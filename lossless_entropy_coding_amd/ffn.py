@@ -287,7 +287,7 @@ def linear(x, w, bias=None, *, act=None, residual=None, x_scale=None, w_scale=No
 @_placed
 def grouped_linear(x, w, offsets, bias=None, *, act=None, residual=None, x_scale=None, w_scale=None, out_scale=None,
                    out_dtype=None, save_preact=False, out=None, preact=None, status=None):
-    """``linear`` by expert: rows offsets[e] .. offsets[e + 1) - 1 of x go
+    """``linear`` by expert: rows offsets[e] .. offsets[e + 1] - 1 of x go
     through w[e] ([groups, n, k]), bias[e] and w_scale[e].
 
     offsets is an int32 CUDA tensor of groups + 1 entries that never
