@@ -517,14 +517,15 @@ int bf16_exp_decode(const uint8_t *d_in, uint64_t in_len, uint16_t *d_out, uint6
  * products with a fused epilogue, dense or grouped by expert, and layer norm,
  * each with its backward pass.  Tensors are row-major with a row stride in
  * elements; a row's elements are contiguous.  Row strides, and pointers down
- * to the element's own alignment, are free; 16-byte aligned pointers with row
- * strides and row lengths that are multiples of 16 bytes are read in place,
- * any other factor of a product is first copied into the workspace (rows
+ * to the element's own alignment, are free.  16-byte aligned pointers with row
+ * strides and row lengths that are multiples of 16 bytes are read in place.
+ * Any other factor of a product is first copied into the workspace (rows
  * padded to 16 bytes), and so is one whose row stride passes 8 to 64 MiB (by
- * tile and direction).  Neither is a factor of a forward product of at most
- * 32 rows (on average by group), which reads rows at any address.  Sizes up
- * to 2^31 - 1; the backward products return EC_E_UNSUPPORTED for longer rows
- * than they say.
+ * tile and direction).  A forward product of at most 32 rows (on average by
+ * group) reads rows at any address, without a copy.  Sizes up to 2^31 - 1; a
+ * product returns EC_E_UNSUPPORTED for longer rows than its direction allows
+ * (see there), for copies of 64 GiB or more, and for more than 2^31 - 256
+ * columns or as many tiles.
  * ------------------------------------------------------------------------- */
 
 typedef enum ec_dtype {

@@ -810,12 +810,12 @@ enum ShapeId { kHuge, kEven, kSmall, kFew };
 // what a workgroup costs besides its stages; bf16 and e4m3.  The full rates
 // are 1.25, 0.87 and 0.51 PFLOP/s in bf16.
 struct ShapeCost {
-    uint32_t TI, TJ, per_cu;
+    uint32_t TI, TJ, threads, per_cu;
     float alone[2], full[2], fixed;
 };
-constexpr ShapeCost kCost[] = {{256, 256, 1, {0.55f, 1.1f}, {0.86f, 1.5f}, 10.0f},
-                               {128, 128, 2, {0.25f, 0.43f}, {0.31f, 0.45f}, 5.0f},
-                               {64, 64, 3, {0.17f, 0.28f}, {0.133f, 0.18f}, 6.0f}};
+constexpr ShapeCost kCost[] = {{256, 256, Huge::THREADS, 1, {0.55f, 1.1f}, {0.86f, 1.5f}, 10.0f},
+                               {128, 128, Even::THREADS, 2, {0.25f, 0.43f}, {0.31f, 0.45f}, 5.0f},
+                               {64, 64, Small::THREADS, 3, {0.17f, 0.28f}, {0.133f, 0.18f}, 6.0f}};
 constexpr uint64_t kCUs = 256;
 
 struct Plan {
@@ -823,7 +823,7 @@ struct Plan {
     uint32_t row_tiles, waves;              // kFew
     uint64_t blocks;
     uint32_t a_pitch, b_pitch;              // elements; 0: read in place
-    bool none;                              // rows too long for every shape
+    bool none;                              // rows too long, or tiles too many, for every shape
     uint64_t a_at, b_at, partial_at, bytes; // workspace
 };
 
@@ -839,6 +839,10 @@ bool aligned(const void *p, uint64_t stride, uint64_t group, uint64_t cols, uint
 bool reachable(uint64_t T, uint64_t stride, uint32_t es, bool outer) {
     return (outer ? kStageBytes / es : T) * stride * es + 65536 < (1ull << 31);
 }
+
+// A launch has fewer than 2^32 threads; of one with more, only the rest by
+// 2^32 would run, without an error.
+bool launchable(uint64_t blocks, uint64_t threads) { return blocks * threads < (1ull << 32); }
 
 Plan make_plan(const ProductArgs &a) {
     Plan q;
@@ -861,6 +865,7 @@ Plan make_plan(const ProductArgs &a) {
         // (16.4 us; 16.2 with eight), with 128 eight are better (13.4, 16.1).
         q.waves = (ragged ? groups : q.tiles_i) * q.tiles_j >= 2 * kCUs ? 4 : 8;
         q.blocks = (uint64_t)q.tiles_i * q.tiles_j;
+        return launchable(q.blocks, q.waves * 64);
     };
     // Few rows a group, forward: one row by 16384 x 2048 weights takes 13.5 us
     // so, 20 us in tiles with a split contraction and its join.  17 to 32 rows:
@@ -875,8 +880,7 @@ Plan make_plan(const ProductArgs &a) {
     const uint64_t rows = ragged ? ceil_div(a.I, groups) : a.I;
     if (a.op == EC_LINEAR_FORWARD && rows <= 32) {
         const bool fill = ceil_div(a.J, 16) * groups >= (ragged ? 2 : 1) * kCUs;
-        few(rows > 16 && fill ? 2 : 1);
-        return q;
+        if (few(rows > 16 && fill ? 2 : 1)) return q;
     }
     // The tiles and the number of splits with the least time, of the shapes
     // whose tiles reach their rows: where these lie, or else in a copy.
@@ -898,11 +902,14 @@ Plan make_plan(const ProductArgs &a) {
             copy_b = !b_aligned || !reachable(c.TJ, b_stride, es, outer_b);
             if ((copy_a && !reachable(c.TI, a_pitch, es, outer_a)) || (copy_b && !reachable(c.TJ, b_pitch, es, outer_b)))
                 continue;
+            if (!launchable(((copy_a ? a_bytes : 0) + (copy_b ? b_bytes : 0)) / 16 + 512, 1)) continue;
             copies = ((copy_a && a_aligned ? a_bytes : 0) + (copy_b && b_aligned ? b_bytes : 0)) * 0.5e-6f;
         }
         const uint64_t ti = ragged ? a.I / c.TI + (groups + 1) / 2 : ceil_div(a.I, c.TI);
         const uint64_t tiles = ti * ceil_div(a.J, c.TJ) * (outer_a ? groups : 1);
-        for (uint32_t n = 1; n == 1 || (!a.groups && n <= 32 && stages / n >= 8); n *= 2) {
+        if (!launchable(most_tiles(c.TI) * ceil_div(a.J, c.TJ) * (outer_a ? groups : 1), c.threads)) continue;
+        for (uint32_t n = 1; n == 1 || (!a.groups && n <= 32 && stages / n >= 8 && launchable(tiles * n, c.threads));
+             n *= 2) {
             const uint64_t rounds = ceil_div(tiles * n, kCUs * c.per_cu), each = ceil_div(stages, n);
             const float alone = rounds * c.alone[es == 1], full = ceil_div(tiles * n, kCUs) * c.full[es == 1];
             float t = (alone > full ? alone : full) * each + c.fixed * rounds + copies;
@@ -917,10 +924,7 @@ Plan make_plan(const ProductArgs &a) {
         }
     }
     if (!best) {                                        // rows of more than 32 MiB
-        if (a.op == EC_LINEAR_FORWARD)
-            few(2);
-        else
-            q.none = true;
+        q.none = a.op != EC_LINEAR_FORWARD || !few(2);
         return q;
     }
     uint64_t at = q.a_pitch ? a_bytes : 0;
@@ -1001,7 +1005,7 @@ hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s) {
     if (!a.I || !a.J)
         return launch_check_offsets(a.offsets, a.groups, a.op == EC_LINEAR_GRAD_WEIGHT ? a.C : a.I, a.status, s);
     const Plan q = make_plan(a);
-    if (q.none || q.blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (q.none) return hipErrorInvalidValue;
     const uint32_t es = a.dtype == EC_E4M3 ? 1 : 2;
     const bool outer_a = a.op == EC_LINEAR_GRAD_WEIGHT, outer_b = a.op != EC_LINEAR_FORWARD;
     char *ws = (char *)workspace;
@@ -1020,7 +1024,7 @@ hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s) {
         a.b_group = rows * q.b_pitch;
     }
     const uint64_t copies = (uint64_t)ca.blocks + cb.blocks;
-    if (copies > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(copies, 256)) return hipErrorInvalidValue;
     if (copies && es == 1)
         copy_rows_kernel<uint8_t><<<(uint32_t)copies, 256, 0, s>>>(ca, cb);
     else if (copies)
@@ -1058,6 +1062,8 @@ hipError_t launch_column_sum(const ColumnSumArgs &a, float *workspace, hipStream
     if (!a.n) return launch_check_offsets(a.offsets, a.groups, a.m, a.status, s);
     const uint32_t parts = column_parts(a), groups = a.groups ? a.groups : 1;
     const uint64_t n = (uint64_t)groups * a.n;
+    if (!launchable(ceil_div(a.n, kSumCols), 256) || (parts > 1 && !launchable(ceil_div(n, 256), 256)))
+        return hipErrorInvalidValue;
     column_sum_kernel<<<dim3((uint32_t)ceil_div(a.n, kSumCols), groups, parts), 256, 0, s>>>(a, parts > 1 ? workspace : a.db,
                                                                                            parts);
     if (parts > 1) column_join_kernel<<<(uint32_t)ceil_div(n, 256), 256, 0, s>>>(workspace, a.db, n, parts);

@@ -162,3 +162,34 @@ def test_more_than_2_30_tokens(ec):
                                    dw_dtype=torch.float32)
     R.near(dw, *R.grad_weight(dy[-last:], x[-last:], torch.float32), "dw")
     R.near(db, *R.column_sum(dy[-last:]), "db")
+
+
+def test_launches_too_large_are_refused(ec):
+    """A launch has fewer than 2^32 threads: 512 for each 256 columns here."""
+    f = ec.lib().linear_forward
+    assert f(ctypes.byref(_args(1, (1 << 31) - 1, 8)), None) == UNSUPPORTED
+    a = _args(40, 1 << 30, 40)
+    a.w = a.w + 2                                   # a copy of 80 GiB
+    assert f(ctypes.byref(a), None) == UNSUPPORTED and _workspace(ec, a, FORWARD) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 20])
+def test_many_columns(ec, m):
+    """More columns than the kernel for few rows can be launched for."""
+    print("many columns %d" % m, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(m)
+    n, k = 300_000_001, 8
+    x = torch.randn(m, k, generator=g, device="cuda").bfloat16()
+    w = torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
+    for lo in range(0, n, 1 << 24):
+        hi = min(n, lo + (1 << 24))
+        w[lo:hi] = torch.randn(hi - lo, k, generator=g, device="cuda").bfloat16()
+    y = ec.linear(x, w)
+    for lo in (0, (1 << 28) - 5000, n - 20000, n // 2):
+        s = slice(lo, lo + 20000)
+        want, tol, _, _ = R.linear(x, w[s])
+        R.near(y[:, s], want, tol, "y from column %d" % lo)
+    for lo in range(0, n, 1 << 24):                 # every column was written: by a float product, roughly
+        hi = min(n, lo + (1 << 24))
+        assert torch.allclose(y[:, lo:hi].float(), x.float() @ w[lo:hi].float().t().contiguous(), rtol=0.05, atol=0.05)
