@@ -57,7 +57,7 @@ def test_long_rows_are_not_copied(ec, m, n, k, dtype):
 
 
 def test_strides_within_reach_are_read_in_place(ec):
-    a = _args(512, 512, 512, x_stride=1 << 22, w_stride=1 << 22)     # 8 MiB: 512 bytes a row would be copied
+    a = _args(512, 512, 512, x_stride=1 << 22, w_stride=1 << 22)     # 8 MiB a row, 512 rows: read in place by tiles of 128
     assert _workspace(ec, a, FORWARD) in (0,) + tuple(s * 512 * 512 * 4 for s in (2, 4, 8, 16, 32))
     a = _args(512, 512, 512, dy_stride=1 << 24, x_stride=1 << 24)     # 32 rows of 32 MiB
     assert _workspace(ec, a, GRAD_WEIGHT) in tuple(s * 512 * 512 * 4 for s in (0, 2, 4, 8, 16, 32))
