@@ -93,6 +93,7 @@ typedef enum ec_error {
                                        bits (or a count is 2^55 or more); the table is unusable
                                        (codec 0) and encodes that use it set this bit too */
 #define EC_S_BAD_OFFSETS 0x20u      /* grouped product: row offsets decrease or leave [0, m] */
+#define EC_S_BAD_TARGET 0x40u       /* cross entropy: a target outside the vocabulary that is not ignore_index */
 
 typedef enum ec_codec {
     EC_CODEC_QLC = 1,
@@ -662,6 +663,131 @@ int layer_norm_grad(const void *d_dy, uint64_t dy_stride, const void *d_x, uint6
                     const void *d_weight, uint32_t w_dtype, const void *d_dres, uint64_t dres_stride, void *d_dx,
                     uint64_t dx_stride, float *d_dweight, float *d_dbias, void *d_workspace,
                     uint64_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward block: both projections, the activation and the
+ * product in one launch, dense or by expert.  Arguments as of the products
+ * above, but w, bias and w_scale have 2 n rows (entries), the gate's n and
+ * then the n of the factor that it multiplies: w [2n, k] ([groups, 2n, k]),
+ * bias [2n], w_scale [1] or [2n], preact [m, 2n]; y is [m, n].  n up to
+ * 2^30 - 1; no residual.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * z[m, 2n] = x_scale[m] w_scale[2n] sum_k x[m, k] w[2n, k] + bias[2n]
+ * preact   = bf16(z)                                   (when d_preact)
+ * y[m, j]  = out_dtype(act(z[m, j]) z[m, n + j])       (EC_E4M3: times *d_out_scale, saturating, ties to even)
+ */
+uint64_t gated_linear_workspace_bytes(const ec_linear_args *a);
+int gated_linear_forward(const ec_linear_args *a, hipStream_t stream);
+
+/*
+ * With g, u = the halves of preact (bf16 [m, 2n]) and dy bf16 [m, n]:
+ *   dz = [dy u act'(g), dy act(g)]
+ *   dx[m, k]  = sum_j dz[m, j] w[j, k]      (bf16, when d_dx; reads d_w)
+ *   dw[2n, k] = sum_m dz[m, j] x[m, k]      (out_dtype EC_BF16 or EC_FP32, when d_dw; reads d_x)
+ *   db[2n]    = sum_m dz[m, j]              (fp32, when d_db; of dz before its rounding)
+ * dz is rounded to bf16 for the two products and lies in the workspace.  n up
+ * to 2^23 - 512, k up to 2^25 - 2048.  Outputs overlap nothing that is read.
+ */
+uint64_t gated_linear_grad_workspace_bytes(const ec_linear_args *a);
+int gated_linear_grad(const ec_linear_args *a, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Softmax cross entropy over a vocabulary of n entries, from rows x [m, k] and
+ * the vocabulary's weights w [n, k] (bf16): the logits l = x w^T are never
+ * kept.  target [m] is int32 or int64; rows whose target is ignore_index have
+ * loss 0 and no gradient, whatever x holds there.  So have rows whose target is
+ * outside [0, n), which also set EC_S_BAD_TARGET in *d_status.
+ * ------------------------------------------------------------------------- */
+typedef struct ec_loss_args {
+    uint64_t m, n, k;
+    const void *d_x;
+    uint64_t x_stride;
+    const void *d_w;
+    uint64_t w_stride;
+    const void *d_target;
+    uint32_t target_bytes;         /* 4: int32, 8: int64 */
+    uint32_t dlosses;              /* dloss entries: 1 (of every row), or m */
+    int64_t ignore_index;
+    float *d_loss;                 /* fp32 [m], written by linear_cross_entropy */
+    float *d_lse;                  /* fp32 [m], written by linear_cross_entropy (or NULL), read by its backward pass */
+    const float *d_dloss;          /* fp32 */
+    void *d_dx;                    /* bf16 [m, k], or NULL */
+    uint64_t dx_stride;
+    void *d_dw;                    /* [n, k], or NULL */
+    uint64_t dw_stride;
+    uint32_t dw_dtype;             /* EC_BF16 or EC_FP32 */
+    uint32_t reserved;
+    uint32_t *d_status;            /* or NULL */
+    void *d_workspace;             /* 16-byte aligned */
+    uint64_t workspace_bytes;
+} ec_loss_args;
+
+/*
+ * lse[m]  = log sum_v exp(l[m, v])
+ * loss[m] = lse[m] - l[m, target[m]]
+ * Products and sums in fp32.
+ */
+uint64_t linear_cross_entropy_workspace_bytes(const ec_loss_args *a);
+int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream);
+
+/*
+ * With G[m, v] = (exp(l[m, v] - lse[m]) - [v = target[m]]) dloss[m]:
+ *   dx[m, k] = sum_v G[m, v] w[v, k]        (bf16)
+ *   dw[v, k] = sum_m G[m, v] x[m, k]        (dw_dtype)
+ * The logits are computed again by pieces of the vocabulary; a piece's G is
+ * rounded to bf16 for the products and lies in the workspace (256 MiB, or 8 KiB
+ * a row where that is more), beside x and the fp32 sums of dx.  Fixed order of
+ * summation.  k up to 2^24 - 1024.
+ */
+uint64_t linear_cross_entropy_grad_workspace_bytes(const ec_loss_args *a);
+int linear_cross_entropy_grad(const ec_loss_args *a, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * AdamW over many tensors at once (decoupled weight decay).
+ *   g = grad * *d_grad_scale,  t = *d_steps + 1
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32; then copy = bf16(p) where given, and *d_steps = t.
+ *
+ * The states of all tensors lie in d_m and d_v, in blocks of EC_ADAMW_BLOCK
+ * values: tensor i's begin at the sum of adamw_state_blocks(n) of those before
+ * it, what its last block holds past its end is zero and stays so.  With
+ * state_dtype EC_E4M3 a block's m is e4m3 times m_scale[block], and v the
+ * square of e4m3 times v_scale[block]; the scales are the least powers of two,
+ * 2^-60 at least, that take the block's values to at most 448.  Both are
+ * rounded up or down at random so that their means are kept, by bits that are
+ * a function of seed, t and the value's place.  Values that are not finite
+ * become NaN.
+ * ------------------------------------------------------------------------- */
+#define EC_ADAMW_BLOCK 256
+
+typedef struct ec_adamw_tensor {
+    float *d_param;                /* fp32 [n] */
+    const void *d_grad;            /* [n] of grad_dtype */
+    uint16_t *d_copy;              /* bf16 [n], or NULL */
+    uint64_t n;
+    uint32_t grad_dtype;           /* EC_BF16 or EC_FP32 */
+    float weight_decay;
+} ec_adamw_tensor;
+
+typedef struct ec_adamw_args {
+    void *d_m, *d_v;               /* state_blocks * 256 values, 16-byte aligned */
+    float *d_m_scale, *d_v_scale;  /* EC_E4M3: [state_blocks] */
+    uint64_t state_blocks;
+    int32_t *d_steps;              /* steps done */
+    const float *d_lr;             /* read instead of lr, or NULL */
+    const float *d_grad_scale;     /* or NULL: 1 */
+    double lr, beta1, beta2, eps;
+    uint32_t state_dtype;          /* EC_FP32 or EC_E4M3 */
+    uint32_t seed;
+} ec_adamw_args;
+
+uint64_t adamw_state_blocks(uint64_t n);
+
+/* tensors: host memory, read before the call returns. */
+int adamw_step(const ec_adamw_tensor *tensors, uint32_t count, const ec_adamw_args *a, hipStream_t stream);
 
 /* Static text for an ec_error value or for a set of EC_S_* status bits. */
 const char *ec_error_string(int code);

@@ -7,7 +7,9 @@ streams.  There is no CPU fallback: if ``libec.so`` is missing the import of
 an entry point raises.
 
 The operators of feed-forward layers (``linear``, ``grouped_linear``,
-``layer_norm`` and their backward passes) are bound in ``ffn``.
+``gated_linear``, ``layer_norm`` and their backward passes) are bound in
+``ffn``, those around them in a training step (``linear_cross_entropy``,
+``adamw``) in ``training``.
 """
 
 from __future__ import annotations
@@ -27,14 +29,15 @@ __all__ = [
     "bf16_exp_table_from_counts", "bf16_exp_table_from_sigma", "bf16_exp_max_encoded_bytes", "bf16_exp_encode",
     "bf16_exp_decode", "byte_histogram_sized", "encode_sized", "encode_batch_sized",
     "linear", "linear_backward", "grouped_linear", "grouped_linear_backward", "layer_norm", "layer_norm_backward",
-    "S_BAD_OFFSETS",
+    "S_BAD_OFFSETS", "gated_linear", "gated_linear_backward", "grouped_gated_linear", "grouped_gated_linear_backward",
+    "linear_cross_entropy", "linear_cross_entropy_backward", "AdamWState", "adamw_state", "adamw", "S_BAD_TARGET",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libec.so")
 
 CODEC_QLC, CODEC_HUFFMAN, CODEC_EXP_GOLOMB = 1, 2, 3
 S_CAPACITY, S_CORRUPT, S_BAD_HEADER, S_CODEBOOK_MISMATCH, S_BAD_CODEBOOK = 0x1, 0x2, 0x4, 0x8, 0x10
-S_BAD_OFFSETS = 0x20
+S_BAD_OFFSETS, S_BAD_TARGET = 0x20, 0x40
 MAX_BATCH = 128
 
 # QLC area layouts (symbols per area, suffix bits per area)
@@ -97,6 +100,16 @@ EXPORTS = {
     "layer_norm_grad_workspace_bytes": (_u64, [_u64, _u64]),
     "layer_norm_grad": (_int, [_vp, _u64, _vp, _u64, _u32, _u64, _u64, _vp, _vp, _vp, _u32, _vp, _u64, _vp, _u64,
                                _vp, _vp, _vp, _u64, _vp]),
+    "gated_linear_workspace_bytes": (_u64, [_vp]),
+    "gated_linear_forward": (_int, [_vp, _vp]),
+    "gated_linear_grad_workspace_bytes": (_u64, [_vp]),
+    "gated_linear_grad": (_int, [_vp, _vp]),
+    "linear_cross_entropy_workspace_bytes": (_u64, [_vp]),
+    "linear_cross_entropy": (_int, [_vp, _vp]),
+    "linear_cross_entropy_grad_workspace_bytes": (_u64, [_vp]),
+    "linear_cross_entropy_grad": (_int, [_vp, _vp]),
+    "adamw_state_blocks": (_u64, [_u64]),
+    "adamw_step": (_int, [_vp, _u32, _vp, _vp]),
     "ec_error_string": (ctypes.c_char_p, [_int]),
     "ec_status_string": (ctypes.c_char_p, [_u32]),
 }
@@ -598,5 +611,6 @@ def pmf_kl(p_counts: torch.Tensor, q_counts: torch.Tensor, q_add: int = 0, out: 
     return out
 
 
-from .ffn import (grouped_linear, grouped_linear_backward, layer_norm, layer_norm_backward, linear,  # noqa: E402
-                  linear_backward)
+from .ffn import (gated_linear, gated_linear_backward, grouped_gated_linear, grouped_gated_linear_backward,  # noqa: E402
+                  grouped_linear, grouped_linear_backward, layer_norm, layer_norm_backward, linear, linear_backward)
+from .training import (AdamWState, adamw, adamw_state, linear_cross_entropy, linear_cross_entropy_backward)  # noqa: E402

@@ -19,7 +19,7 @@ OBJ = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libec.so")
 
 SOURCES = ["api.hip", "encode.hip", "decode.hip", "histogram.hip", "build.hip", "bf16exp.hip", "ffn_api.hip", "product.hip",
-           "norm.hip", "codebook.cpp"]
+           "gated.hip", "loss.hip", "norm.hip", "adamw.hip", "codebook.cpp"]
 
 ARCH = "gfx950"
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"

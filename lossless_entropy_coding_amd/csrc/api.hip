@@ -299,6 +299,7 @@ const char *ec_status_string(uint32_t st) {
     if (st & EC_S_CORRUPT) return "corrupt stream";
     if (st & EC_S_CAPACITY) return "output capacity exceeded";
     if (st & EC_S_BAD_OFFSETS) return "row offsets of a grouped product decrease or leave the rows";
+    if (st & EC_S_BAD_TARGET) return "a target outside the vocabulary that is not the ignored one";
     return "unknown status";
 }
 

@@ -1,7 +1,9 @@
-// C ABI of the feed-forward operators: argument checks and launches.
+// C ABI of the feed-forward operators, the loss and the weight update: argument checks and launches.
+#include <math.h>
 #include <string.h>
 
 #include "ffn_common.h"
+#include "train_common.h"
 
 namespace ec {
 namespace {
@@ -324,4 +326,290 @@ int layer_norm_grad(const void *d_dy, uint64_t dy_stride, const void *d_x, uint6
     a.partial = d_dweight || d_dbias ? (float *)d_workspace : nullptr;
     a.parts = norm_grad_parts(rows, cols);
     return hip_code(launch_norm_grad(a, stream));
+}
+
+// ------------------------------------------------------------------ gated block
+
+namespace {
+
+// w and bias have 2 n rows; so does preact 2 n columns.
+int check_gated(const ec_linear_args *a) {
+    if (!common_ok(a) || a->n > kMaxSize / 2) return EC_E_INVAL;
+    const uint64_t n = a->n, rows = 2 * n;
+    if (a->dtype != EC_BF16 && a->dtype != EC_E4M3) return EC_E_INVAL;
+    if (!size_of(a->out_dtype) || a->d_residual) return EC_E_INVAL;
+    if (!factor_ok(a->d_x, a->dtype, a->m, a->k, a->x_stride)) return EC_E_INVAL;
+    if (!factor_ok(a->d_w, a->dtype, rows, a->k, a->w_stride)) return EC_E_INVAL;
+    if (!group_stride_ok(a, rows, a->k, a->w_stride, a->w_group_stride)) return EC_E_INVAL;
+    if (!factor_ok(a->d_y, a->out_dtype, a->m, n, a->y_stride)) return EC_E_INVAL;
+    if (a->d_bias && ((a->bias_dtype != EC_BF16 && a->bias_dtype != EC_FP32) ||
+                      !tensor_ok(a->d_bias, a->bias_dtype, 1, rows, rows)))
+        return EC_E_INVAL;
+    if (!tensor_ok(a->d_preact, EC_BF16, a->m, rows, a->d_preact ? a->preact_stride : rows)) return EC_E_INVAL;
+    if (a->d_x_scale && a->x_scales != 1 && a->x_scales != a->m) return EC_E_INVAL;
+    if (a->d_w_scale && a->w_scales != 1 && a->w_scales != rows) return EC_E_INVAL;
+    if (((uintptr_t)a->d_x_scale | (uintptr_t)a->d_w_scale | (uintptr_t)a->d_out_scale) & 3) return EC_E_INVAL;
+    if (a->d_out_scale && a->out_dtype != EC_E4M3) return EC_E_INVAL;
+    return EC_OK;
+}
+
+int check_gated_grad(const ec_linear_args *a) {
+    if (!common_ok(a) || a->n > kMaxSize / 2 || a->dtype != EC_BF16) return EC_E_INVAL;
+    const uint64_t n = a->n, rows = 2 * n;
+    if (!factor_ok(a->d_dy, EC_BF16, a->m, n, a->dy_stride)) return EC_E_INVAL;
+    if (!factor_ok(a->d_preact, EC_BF16, a->m, rows, a->preact_stride)) return EC_E_INVAL;
+    if (a->d_dx) {
+        if (!factor_ok(a->d_w, EC_BF16, rows, a->k, a->w_stride)) return EC_E_INVAL;
+        if (!group_stride_ok(a, rows, a->k, a->w_stride, a->w_group_stride)) return EC_E_INVAL;
+        if (!tensor_ok(a->d_dx, EC_BF16, a->m, a->k, a->dx_stride)) return EC_E_INVAL;
+    }
+    if (a->d_dw) {
+        if (a->out_dtype != EC_BF16 && a->out_dtype != EC_FP32) return EC_E_INVAL;
+        if (!factor_ok(a->d_x, EC_BF16, a->m, a->k, a->x_stride)) return EC_E_INVAL;
+        if (!tensor_ok(a->d_dw, a->out_dtype, rows, a->k, a->dw_stride)) return EC_E_INVAL;
+        if (!group_stride_ok(a, rows, a->k, a->dw_stride, a->dw_group_stride)) return EC_E_INVAL;
+    }
+    return ((uintptr_t)a->d_db & 3) == 0 ? EC_OK : EC_E_INVAL;
+}
+
+ProductArgs gated_product(const ec_linear_args *a) {
+    ProductArgs p = product(a, EC_LINEAR_FORWARD);
+    p.op = kOpGated;
+    p.b_j = row_stride(2 * a->n, a->k, a->w_stride, a->dtype);
+    return p;
+}
+
+// The backward pass: where dz and the sums' parts lie, and its two products.
+struct GatedGrad {
+    GatedGradArgs grad;
+    ProductArgs dx, dw;
+    uint64_t partial, product, bytes;       // workspace
+};
+
+GatedGrad gated_grad(const ec_linear_args *a, void *workspace) {
+    GatedGrad q;
+    memset(&q, 0, sizeof(q));
+    char *ws = (char *)workspace;
+    GatedGradArgs &g = q.grad;
+    g.dy = (const uint16_t *)a->d_dy;
+    g.dy_stride = a->dy_stride;
+    g.preact = (const uint16_t *)a->d_preact;
+    g.preact_stride = a->preact_stride;
+    g.m = (uint32_t)a->m;
+    g.n = (uint32_t)a->n;
+    g.groups = a->groups;
+    g.act = a->act;
+    g.offsets = a->d_offsets;
+    g.status = a->d_status;
+    g.dz = (uint16_t *)ws;
+    g.pitch = (2 * a->n + 7) / 8 * 8;
+    g.db = a->d_db;
+    const uint32_t parts = gated_grad_parts(g);
+    q.partial = (a->m * g.pitch * 2 + 255) / 256 * 256;
+    q.product = q.partial;
+    if (a->d_db && parts > 1) q.product += ((uint64_t)parts * (a->groups ? a->groups : 1) * 2 * a->n * 4 + 255) / 256 * 256;
+    g.partial = (float *)(ws + q.partial);
+    q.bytes = q.product;
+    // the products of dz, as of the gradient of a product with 2 n columns
+    ec_linear_args l = *a;
+    l.n = 2 * a->n;
+    l.act = EC_ACT_NONE;
+    l.d_dy = g.dz;
+    l.dy_stride = g.pitch;
+    l.d_preact = nullptr;
+    l.d_db = nullptr;
+    l.d_status = nullptr;
+    if (a->d_dx) {
+        q.dx = product(&l, EC_LINEAR_GRAD_INPUT);
+        q.dx.a_i = g.pitch;
+        q.dx.a_padded = true;
+        const uint64_t need = q.product + product_workspace(q.dx);
+        q.bytes = need > q.bytes ? need : q.bytes;
+    }
+    if (a->d_dw) {
+        q.dw = product(&l, EC_LINEAR_GRAD_WEIGHT);
+        q.dw.a_c = g.pitch;
+        const uint64_t need = q.product + product_workspace(q.dw);
+        q.bytes = need > q.bytes ? need : q.bytes;
+    }
+    return q;
+}
+
+bool runs(const GatedGrad &q, const ec_linear_args *a) {
+    return (!a->d_dx || product_fits(q.dx)) && (!a->d_dw || product_fits(q.dw));
+}
+
+}  // namespace
+
+uint64_t gated_linear_workspace_bytes(const ec_linear_args *a) {
+    if (check_gated(a)) return 0;
+    return product_workspace(gated_product(a));
+}
+
+int gated_linear_forward(const ec_linear_args *a, hipStream_t stream) {
+    const int rc = check_gated(a);
+    if (rc) return rc;
+    const ProductArgs p = gated_product(a);
+    if (!product_fits(p)) return EC_E_UNSUPPORTED;
+    const uint64_t need = product_workspace(p);
+    if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;
+    return hip_code(launch_gated(p, a->d_workspace, stream));
+}
+
+uint64_t gated_linear_grad_workspace_bytes(const ec_linear_args *a) {
+    if (check_gated_grad(a)) return 0;
+    const GatedGrad q = gated_grad(a, nullptr);
+    return runs(q, a) ? q.bytes : 0;
+}
+
+int gated_linear_grad(const ec_linear_args *a, hipStream_t stream) {
+    const int rc = check_gated_grad(a);
+    if (rc) return rc;
+    const GatedGrad q = gated_grad(a, a->d_workspace);
+    if (!runs(q, a)) return EC_E_UNSUPPORTED;
+    if (q.bytes && (!a->d_workspace || a->workspace_bytes < q.bytes)) return EC_E_INVAL;
+    hipError_t e = launch_gated_grad(q.grad, stream);
+    char *const ws = (char *)a->d_workspace + q.product;
+    if (e == hipSuccess && a->d_dx) e = launch_product(q.dx, ws, stream);
+    if (e == hipSuccess && a->d_dw) e = launch_product(q.dw, ws, stream);
+    return hip_code(e);
+}
+
+// --------------------------------------------------------------- cross entropy
+
+namespace {
+
+bool loss_ok(const ec_loss_args *a) {
+    if (!a || a->m > kMaxSize || !a->n || a->n > kMaxSize || a->k > kMaxSize) return false;
+    if (a->target_bytes != 4 && a->target_bytes != 8) return false;
+    if (!factor_ok(a->d_x, EC_BF16, a->m, a->k, a->x_stride) || !factor_ok(a->d_w, EC_BF16, a->n, a->k, a->w_stride))
+        return false;
+    if (a->m && (!a->d_target || ((uintptr_t)a->d_target & (a->target_bytes - 1)))) return false;
+    return !(((uintptr_t)a->d_lse | (uintptr_t)a->d_status) & 3) && !((uintptr_t)a->d_workspace & 15);
+}
+
+LossArgs loss_args(const ec_loss_args *a) {
+    LossArgs p;
+    memset(&p, 0, sizeof(p));
+    p.x = a->d_x;
+    p.x_stride = row_stride(a->m, a->k, a->x_stride, EC_BF16);
+    p.w = a->d_w;
+    p.w_stride = row_stride(a->n, a->k, a->w_stride, EC_BF16);
+    p.m = (uint32_t)a->m;
+    p.n = (uint32_t)a->n;
+    p.k = (uint32_t)a->k;
+    p.target = a->d_target;
+    p.target_bytes = a->target_bytes;
+    p.ignore = a->ignore_index;
+    p.loss = a->d_loss;
+    p.lse = a->d_lse;
+    p.dloss = a->d_dloss;
+    p.dlosses = a->dlosses;
+    p.dx = a->d_dx;
+    p.dx_stride = a->dx_stride;
+    p.dw = a->d_dw;
+    p.dw_stride = a->dw_stride;
+    p.dw_dtype = a->dw_dtype;
+    p.status = a->d_status;
+    return p;
+}
+
+int check_loss(const ec_loss_args *a) {
+    if (!loss_ok(a) || (a->m && !a->d_loss) || ((uintptr_t)a->d_loss & 3)) return EC_E_INVAL;
+    return EC_OK;
+}
+
+int check_loss_grad(const ec_loss_args *a) {
+    if (!loss_ok(a) || (a->m && (!a->d_lse || !a->d_dloss)) || ((uintptr_t)a->d_dloss & 3)) return EC_E_INVAL;
+    if (a->dlosses != 1 && a->dlosses != a->m) return EC_E_INVAL;
+    if (a->d_dx && !tensor_ok(a->d_dx, EC_BF16, a->m, a->k, a->dx_stride)) return EC_E_INVAL;
+    if (a->d_dw && ((a->dw_dtype != EC_BF16 && a->dw_dtype != EC_FP32) ||
+                    !tensor_ok(a->d_dw, a->dw_dtype, a->n, a->k, a->dw_stride)))
+        return EC_E_INVAL;
+    return EC_OK;
+}
+
+}  // namespace
+
+uint64_t linear_cross_entropy_workspace_bytes(const ec_loss_args *a) {
+    if (check_loss(a)) return 0;
+    const LossArgs p = loss_args(a);
+    return loss_fits(p, false) ? loss_workspace(p) : 0;
+}
+
+int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream) {
+    const int rc = check_loss(a);
+    if (rc) return rc;
+    const LossArgs p = loss_args(a);
+    if (!loss_fits(p, false)) return EC_E_UNSUPPORTED;
+    const uint64_t need = loss_workspace(p);
+    if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;
+    return hip_code(launch_loss(p, a->d_workspace, stream));
+}
+
+uint64_t linear_cross_entropy_grad_workspace_bytes(const ec_loss_args *a) {
+    return check_loss_grad(a) ? 0 : loss_grad_workspace(loss_args(a));
+}
+
+int linear_cross_entropy_grad(const ec_loss_args *a, hipStream_t stream) {
+    const int rc = check_loss_grad(a);
+    if (rc) return rc;
+    const LossArgs p = loss_args(a);
+    if (!loss_fits(p, true)) return EC_E_UNSUPPORTED;
+    if (!a->d_workspace || a->workspace_bytes < loss_grad_workspace(p)) return EC_E_INVAL;
+    return hip_code(launch_loss_grad(p, a->d_workspace, stream));
+}
+
+// ----------------------------------------------------------------------- AdamW
+
+uint64_t adamw_state_blocks(uint64_t n) { return adamw_blocks(n); }
+
+int adamw_step(const ec_adamw_tensor *tensors, uint32_t count, const ec_adamw_args *a, hipStream_t stream) {
+    if (!a || (count && !tensors)) return EC_E_INVAL;
+    if (a->state_dtype != EC_FP32 && a->state_dtype != EC_E4M3) return EC_E_INVAL;
+    const bool coded = a->state_dtype == EC_E4M3;
+    if (!a->d_steps || ((uintptr_t)a->d_steps & 3) || (((uintptr_t)a->d_lr | (uintptr_t)a->d_grad_scale) & 3))
+        return EC_E_INVAL;
+    if (!(a->beta1 >= 0.0 && a->beta1 < 1.0 && a->beta2 >= 0.0 && a->beta2 < 1.0 && a->eps >= 0.0)) return EC_E_INVAL;
+    uint64_t blocks = 0;
+    for (uint32_t i = 0; i < count; ++i) {
+        const ec_adamw_tensor &t = tensors[i];
+        if (t.n > (1ull << 40) || (t.grad_dtype != EC_BF16 && t.grad_dtype != EC_FP32)) return EC_E_INVAL;
+        if (t.n && (!t.d_param || !t.d_grad)) return EC_E_INVAL;
+        if (((uintptr_t)t.d_param & 3) || ((uintptr_t)t.d_grad & (t.grad_dtype == EC_BF16 ? 1 : 3)) || ((uintptr_t)t.d_copy & 1))
+            return EC_E_INVAL;
+        blocks += adamw_blocks(t.n);
+    }
+    if (blocks > a->state_blocks) return EC_E_INVAL;
+    if (blocks && (!a->d_m || !a->d_v || (((uintptr_t)a->d_m | (uintptr_t)a->d_v) & 15))) return EC_E_INVAL;
+    if (coded && blocks && (!a->d_m_scale || !a->d_v_scale || (((uintptr_t)a->d_m_scale | (uintptr_t)a->d_v_scale) & 3)))
+        return EC_E_INVAL;
+    AdamArgs p;
+    memset(&p, 0, sizeof(p));
+    p.m = a->d_m;
+    p.v = a->d_v;
+    p.m_scale = a->d_m_scale;
+    p.v_scale = a->d_v_scale;
+    p.steps = a->d_steps;
+    p.lr_at = a->d_lr;
+    p.grad_scale = a->d_grad_scale;
+    p.lr = (float)a->lr;
+    p.b1 = (float)a->beta1;
+    p.b2 = (float)a->beta2;
+    p.rest1 = (float)(1.0 - a->beta1);
+    p.rest2 = (float)(1.0 - a->beta2);
+    p.log_b1 = (float)log(a->beta1);
+    p.log_b2 = (float)log(a->beta2);
+    p.eps = (float)a->eps;
+    p.seed = a->seed;
+    p.e4m3 = coded;
+    AdamBatch batch(p, stream);
+    uint64_t block = 0;
+    hipError_t e = hipSuccess;
+    for (uint32_t i = 0; i < count && e == hipSuccess; ++i) {
+        const ec_adamw_tensor &t = tensors[i];
+        e = batch.add(AdamTensor{t.d_param, t.d_grad, t.d_copy, t.n, block, t.weight_decay, t.grad_dtype == EC_BF16});
+        block += adamw_blocks(t.n);
+    }
+    return hip_code(e == hipSuccess ? batch.finish() : e);
 }

@@ -25,6 +25,22 @@ constexpr float kE4m3Max = 448.0f;
 
 // ------------------------------------------------------------- product launch
 
+// Products beside ec_linear_op's.
+enum ProductOp : uint32_t {
+    kOpGated = 3,       // forward, B's first J rows the gate, the next J what it is multiplied by
+    kOpRowStats,        // forward, of each row of D the maximum and the sum of exponentials only
+    kOpLogitGrad,       // forward, D turned into the gradient of the cross entropy
+    kOpPieceInput,      // grad input over a piece of the contraction, added up in fp32
+    kOpPieceWeight      // grad weight of a piece
+};
+
+constexpr bool contracts_a_rows(uint32_t op) { return op == EC_LINEAR_GRAD_WEIGHT || op == kOpPieceWeight; }
+constexpr bool contracts_b_rows(uint32_t op) {
+    return op == EC_LINEAR_GRAD_INPUT || op == kOpPieceInput || contracts_a_rows(op);
+}
+// Whether the number of rows (of the contraction, in grad weight) is found on the device.
+constexpr bool counts_rows(uint32_t op) { return op >= kOpLogitGrad; }
+
 // One product D[i, j] = sum_c A[i, c] B[j, c] with an epilogue; i are rows of
 // the output, j its contiguous columns, c the contraction:
 //   forward      i = token,         j = output column, c = input column
@@ -34,8 +50,9 @@ constexpr float kE4m3Max = 448.0f;
 struct ProductArgs {
     const void *a, *b;
     uint64_t a_i, a_c, b_j, b_c, b_group;  // b_group: elements between experts' B (forward, grad input)
+    bool a_padded, b_padded;               // A's (B's) rows hold zeros up to a multiple of 16 bytes
     uint32_t I, J, C;
-    uint32_t op;                           // ec_linear_op
+    uint32_t op;                           // ec_linear_op or ProductOp
     uint32_t dtype;                        // EC_BF16 or EC_E4M3
     uint32_t groups;                       // 0: one product
     const int32_t *offsets;                // [groups + 1]: rows i (forward, grad input) or contraction c (grad weight)
@@ -51,6 +68,16 @@ struct ProductArgs {
     uint16_t *preact;                      // written (forward) or read (grad input)
     uint64_t preact_stride;
     float *db;                             // grad weight: [groups][I] sums of A over the contraction, or null
+    // the loss over columns j (kOpRowStats, and by piece the operators after it)
+    const void *target;                    // kOpRowStats: [I] int32 or int64
+    uint32_t target_bytes;
+    float *hit;                            // kOpRowStats: [I] D at the target's column, where that exists
+    float2 *stats;                         // kOpRowStats: [I][tiles_j] maximum, sum of exponentials from it
+    const uint32_t *used;                  // rows that exist, of those the launch has room for
+    const float2 *row;                     // kOpLogitGrad: [I] log of the sum of exponentials, gradient of the loss
+    const int32_t *row_target;             // kOpLogitGrad: [I] the target's column
+    uint32_t first;                        // kOpLogitGrad: the piece's first column
+    const float *sum_in;                   // kOpPieceInput: added to D (as out in type and stride), or null
     // filled in by the plan
     uint32_t tiles_i, tiles_j, splits;
     float *partial;                        // [splits][tile][TI * TJ] when splits > 1
@@ -72,6 +99,52 @@ hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s);
 hipError_t launch_check_offsets(const int32_t *offsets, uint32_t groups, uint32_t m, uint32_t *status, hipStream_t s);
 uint64_t column_sum_workspace(const ColumnSumArgs &a);
 hipError_t launch_column_sum(const ColumnSumArgs &a, float *workspace, hipStream_t s);
+hipError_t launch_column_join(const float *in, float *out, uint64_t n, uint32_t parts, hipStream_t s);
+hipError_t launch_copy_rows(const void *in, uint64_t stride, uint64_t rows, uint64_t cols, uint32_t dtype, void *out,
+                            uint64_t pitch, hipStream_t s);
+
+// The gated product's backward pass up to the products: dz = [dy rest act'(gate), dy act(gate)] from
+// preact = [gate, rest] (n columns each), and the sums of dz's rows before their rounding.
+struct GatedGradArgs {
+    const uint16_t *dy, *preact;
+    uint64_t dy_stride, preact_stride;
+    uint32_t m, n, groups, act;
+    const int32_t *offsets;
+    uint32_t *status;
+    uint16_t *dz;                          // [m, pitch], zeros in columns 2 n ..; rows of no group are left as they are
+    uint64_t pitch;
+    float *db;                             // [groups][2 n], or null
+    float *partial;                        // [parts][groups][2 n] when parts > 1
+};
+
+hipError_t launch_gated(ProductArgs a, void *workspace, hipStream_t s);
+uint32_t gated_grad_parts(const GatedGradArgs &a);
+hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s);
+
+// Cross entropy over the products of x and w, forward and backward.
+struct LossArgs {
+    const void *x, *w;
+    uint64_t x_stride, w_stride;
+    uint32_t m, n, k;
+    const void *target;
+    uint32_t target_bytes;
+    int64_t ignore;
+    float *loss, *lse;                     // lse: read in the backward pass
+    const float *dloss;
+    uint32_t dlosses;                      // 1 or m
+    void *dx;
+    uint64_t dx_stride;
+    void *dw;
+    uint64_t dw_stride;
+    uint32_t dw_dtype;
+    uint32_t *status;
+};
+
+uint64_t loss_workspace(const LossArgs &a);
+uint64_t loss_grad_workspace(const LossArgs &a);
+bool loss_fits(const LossArgs &a, bool grad);
+hipError_t launch_loss(const LossArgs &a, void *workspace, hipStream_t s);
+hipError_t launch_loss_grad(const LossArgs &a, void *workspace, hipStream_t s);
 
 struct NormArgs {
     const void *x;
@@ -188,6 +261,18 @@ __device__ __forceinline__ float act_slope(float z) {
     } else {
         return 1.0f;
     }
+}
+
+// ------------------------------------------------------ sums of exponentials
+
+constexpr float kLog2E = 1.44269504f;
+
+// (maximum, sum of exponentials from it) of two sets of values.  With no value
+// above -inf in either the sum stays 0.
+__device__ __forceinline__ float2 join_stats(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x), from = top == -__builtin_inff() ? 0.0f : top;
+    return float2{top, a.y * __builtin_amdgcn_exp2f((a.x - from) * kLog2E) +
+                           b.y * __builtin_amdgcn_exp2f((b.x - from) * kLog2E)};
 }
 
 // ------------------------------------------------------------- ragged groups
@@ -439,6 +524,13 @@ __device__ __forceinline__ void finish8(const ProductArgs &p, uint32_t g, uint32
         if (p.out_scale) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] *= out_scale;
+        }
+    } else if constexpr (OP == kOpPieceInput) {
+        if (p.sum_in) {
+            float before[8];
+            load8(p.sum_in, EC_FP32, i * p.out_stride + j, c.left, before);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += before[q];
         }
     } else if constexpr (OP == EC_LINEAR_GRAD_INPUT) {
         if constexpr (ACT != EC_ACT_NONE) {

@@ -1,5 +1,6 @@
 """Feed-forward operators: matrix products with a fused epilogue (dense, or
-grouped by expert) and layer norm, forward and backward.
+grouped by expert), the gated block's two products in one, and layer norm,
+forward and backward.
 
 Like the rest of the binding this module checks and marshals arguments; the
 work runs in the library's HIP kernels, asynchronously on the current stream
@@ -375,6 +376,169 @@ def grouped_linear_backward(dy, x, w, offsets, *, preact=None, act=None, need_dx
     if offsets is None:
         _error("offsets must be a tensor")
     return _backward(dy, x, w, offsets, preact, act, need_dx, need_dw, need_db, dw_dtype, dx, dw, db, status)
+
+
+def _gated(x, w, offsets, bias, act, x_scale, w_scale, out_scale, out_dtype, save_preact, out, preact, status):
+    E4 = (torch.float8_e4m3fn, torch.uint8)
+    a = _LinearArgs()
+    a.groups, n2, k, a.w_stride, a.w_group_stride = _weights(w, "w", offsets, (torch.bfloat16,) + E4)
+    if n2 & 1:
+        _error("w must have an even number of rows, the gate's and then as many, not %d" % n2)
+    n, dev = n2 // 2, w.device
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _error("x must be a 2-D CUDA tensor")
+    m = x.shape[0]
+    a.x_stride = _matrix(x, "x", m, k, (torch.bfloat16,) if w.dtype == torch.bfloat16 else E4, dev)
+    a.m, a.n, a.k = m, n, k
+    a.dtype = _DTYPES[w.dtype]
+    a.act = _act(act)
+    a.x, a.w = x.data_ptr(), w.data_ptr()
+    per = (a.groups,) if a.groups else ()
+    if a.groups:
+        a.offsets = offsets.data_ptr()
+        a.status = _status(status, dev)
+    if bias is not None:
+        _vector(bias, "bias", (per + (n2,),), (torch.float32, torch.bfloat16), dev)
+        a.bias, a.bias_dtype = bias.data_ptr(), _DTYPES[bias.dtype]
+    if x_scale is not None:
+        _vector(x_scale, "x_scale", ((1,), (m,)), (torch.float32,), dev)
+        a.x_scale, a.x_scales = x_scale.data_ptr(), x_scale.numel()
+    if w_scale is not None:
+        _vector(w_scale, "w_scale", (per + (1,), per + (n2,)), (torch.float32,), dev)
+        a.w_scale, a.w_scales = w_scale.data_ptr(), w_scale.shape[-1]
+    if out is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
+        if out_dtype not in _DTYPES:
+            _error("out_dtype must be bfloat16, float32, float8_e4m3fn or uint8 (e4m3 bytes), not %s" % out_dtype)
+        out, a.y_stride = _empty((m, n), out_dtype, dev), n
+    else:
+        _given(out, "out", out_dtype)
+        a.y_stride = _matrix(out, "out", m, n, _DTYPES, dev)
+    a.y, a.out_dtype = out.data_ptr(), _DTYPES[out.dtype]
+    if out_scale is not None:
+        if a.out_dtype != _E4M3:
+            _error("out_scale goes with an e4m3 output")
+        _vector(out_scale, "out_scale", ((1,),), (torch.float32,), dev)
+        a.out_scale = out_scale.data_ptr()
+    if save_preact or preact is not None:
+        if preact is None:
+            preact, a.preact_stride = _empty((m, n2), torch.bfloat16, dev), n2
+        else:
+            a.preact_stride = _matrix(preact, "preact", m, n2, (torch.bfloat16,), dev)
+        a.preact = preact.data_ptr()
+    _warn_unrecorded(3, x, w, bias)
+    _run("gated_linear_workspace_bytes", "gated_linear_forward", a, dev)
+    return out if preact is None else (out, preact)
+
+
+def _run(size: str, name: str, args, device):
+    """A call whose workspace another function of the library tells."""
+    ec = _ec()
+    L = ec.lib()
+    need = int(getattr(L, size)(ctypes.byref(args)))
+    if need:  # freed at return, to be used again in the order of this stream
+        ws = _empty(need, torch.uint8, device)
+        args.workspace, args.workspace_bytes = ws.data_ptr(), need
+    ec._check(getattr(L, name)(ctypes.byref(args), ec._stream(None)), name)
+
+
+@_placed
+def gated_linear(x, w, bias=None, *, act="silu", x_scale=None, w_scale=None, out_scale=None, out_dtype=None,
+                 save_preact=False, out=None, preact=None):
+    """y = act(z[:, :n]) * z[:, n:] with z = x w^T * x_scale * w_scale + bias:
+    both projections of a gated feed-forward block, the activation and the
+    product at once.
+
+    x [m, k] and w [2n, k] both bfloat16, or both e4m3; w's first n rows are
+    the gate's.  bias [2n], w_scale [1] or [2n]; otherwise the arguments are
+    those of ``linear``, y [m, n] its result.  Returns y, or (y, preact) with
+    save_preact (or a preact buffer): z [m, 2n] as bfloat16, for the backward
+    pass."""
+    return _gated(x, w, None, bias, act, x_scale, w_scale, out_scale, out_dtype, save_preact, out, preact, None)
+
+
+@_placed
+def grouped_gated_linear(x, w, offsets, bias=None, *, act="silu", x_scale=None, w_scale=None, out_scale=None,
+                         out_dtype=None, save_preact=False, out=None, preact=None, status=None):
+    """``gated_linear`` by expert: w [groups, 2n, k], bias [groups, 2n],
+    w_scale [groups, 1] or [groups, 2n]; offsets and status are those of
+    ``grouped_linear``."""
+    if offsets is None:
+        _error("offsets must be a tensor")
+    return _gated(x, w, offsets, bias, act, x_scale, w_scale, out_scale, out_dtype, save_preact, out, preact, status)
+
+
+def _gated_backward(dy, x, w, offsets, preact, act, need_dx, need_dw, need_db, dw_dtype, dx, dw, db, status):
+    bf = (torch.bfloat16,)
+    a = _LinearArgs()
+    a.groups, n2, k, a.w_stride, a.w_group_stride = _weights(w, "w", offsets, bf)
+    if n2 & 1:
+        _error("w must have an even number of rows, the gate's and then as many, not %d" % n2)
+    n, dev = n2 // 2, w.device
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+        _error("dy must be a 2-D CUDA tensor")
+    m = dy.shape[0]
+    a.m, a.n, a.k, a.dtype, a.act = m, n, k, _BF16, _act(act)
+    a.dy_stride, a.dy = _matrix(dy, "dy", m, n, bf, dev), dy.data_ptr()
+    a.preact_stride, a.preact = _matrix(preact, "preact", m, n2, bf, dev), preact.data_ptr()
+    if a.groups:
+        a.offsets = offsets.data_ptr()
+        a.status = _status(status, dev)
+    per = (a.groups,) if a.groups else ()
+    need_dx, need_dw, need_db = need_dx or dx is not None, need_dw or dw is not None, need_db or db is not None
+    if need_dx:
+        a.w = w.data_ptr()
+        if dx is None:
+            dx, a.dx_stride = _empty((m, k), torch.bfloat16, dev), k
+        else:
+            a.dx_stride = _matrix(dx, "dx", m, k, bf, dev)
+        a.dx = dx.data_ptr()
+    if need_dw:
+        a.x_stride, a.x = _matrix(x, "x", m, k, bf, dev), x.data_ptr()
+        if dw is None:
+            dw = _empty(per + (n2, k), dw_dtype if dw_dtype is not None else torch.bfloat16, dev)
+        else:
+            _given(dw, "dw", dw_dtype)
+        if tuple(dw.shape) != per + (n2, k) or dw.device != dev:
+            _error("dw must be %s on %s" % (list(per + (n2, k)), dev))
+        if dw.dtype not in (torch.bfloat16, torch.float32):
+            _error("dw must be bfloat16 or float32, not %s" % dw.dtype)
+        a.dw_stride, a.dw, a.out_dtype = _row_stride(dw, "dw"), dw.data_ptr(), _DTYPES[dw.dtype]
+        a.dw_group_stride = dw.stride(0) if a.groups > 1 else 0
+    if need_db:
+        if db is None:
+            db = _empty(per + (n2,), torch.float32, dev)
+        else:
+            _vector(db, "db", (per + (n2,),), (torch.float32,), dev)
+        a.db = db.data_ptr()
+    if need_dx or need_dw or need_db:
+        _run("gated_linear_grad_workspace_bytes", "gated_linear_grad", a, dev)
+    return dx, dw, db
+
+
+@_placed
+def gated_linear_backward(dy, x, w, preact, *, act="silu", need_dx=True, need_dw=True, need_db=True, dw_dtype=None,
+                          dx=None, dw=None, db=None):
+    """Gradients of ``gated_linear`` for dy [m, n], from its preact [m, 2n]
+    (all bfloat16).
+
+    Returns (dx, dw, db), None where not needed: dx [m, k] bfloat16, dw
+    [2n, k] in dw_dtype (bfloat16, or float32), db [2n] float32.  The gradient
+    of preact is rounded to bfloat16 for the two products (not for db).  Sums
+    run in a fixed order: the same call gives the same bits."""
+    return _gated_backward(dy, x, w, None, preact, act, need_dx, need_dw, need_db, dw_dtype, dx, dw, db, None)
+
+
+@_placed
+def grouped_gated_linear_backward(dy, x, w, offsets, preact, *, act="silu", need_dx=True, need_dw=True, need_db=True,
+                                  dw_dtype=None, dx=None, dw=None, db=None, status=None):
+    """``gated_linear_backward`` by expert: dw [groups, 2n, k] and db
+    [groups, 2n] hold each expert's sums over its rows (zeros for an empty
+    one); rows of no group get zeros in dx."""
+    if offsets is None:
+        _error("offsets must be a tensor")
+    return _gated_backward(dy, x, w, offsets, preact, act, need_dx, need_dw, need_db, dw_dtype, dx, dw, db, status)
 
 
 def _norm_params(weight, bias, cols, dev):
