@@ -25,8 +25,22 @@ namespace ec {
 namespace {
 
 constexpr uint32_t kBlock = 256;            // values with one scale; a wave's float4 a lane
-constexpr int kWaves = 4, kPerWave = 4;     // blocks a wave has on the way
-constexpr uint32_t kChunk = kWaves * kPerWave;
+constexpr int kPerWave = 4;                 // blocks a wave has on the way
+constexpr int kWaves = 4, kAloneWaves = 16; // a workgroup's
+// Workgroups of a launch; more take several chunks a wave.  A layer of 45
+// million values with fp32 states: 185 us with 4096, 180 with 8192, 186 with
+// 16384.
+constexpr uint32_t kMostBlocks = 8192;
+// Chunks up to which one workgroup does a step alone, the step's number too,
+// which otherwise is a launch of its own: 7 us for 18 chunks, 7 and 5 so.
+constexpr uint32_t kAloneChunks = 32;
+
+// At any address that suits their elements.  Params and states are read and
+// written past the caches (non-temporal), since a step's do not stay there till
+// the next one; the copies, which the next layer reads, are not.  45 million
+// values with fp32 states: 216 us without, 180 with, 191 with the copies too.
+typedef f32x4 AnyFloats __attribute__((aligned(4)));
+typedef u32x2 AnyHalves __attribute__((aligned(2)));
 constexpr int kLeastScale = -60;            // exponent
 constexpr float kRootMax = 448.0f * 448.0f;
 
@@ -41,22 +55,48 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 // 2^e for e in the normal range.
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// The exponent e of the least 2^e with top <= most 2^e, kLeastScale at least;
-// top is finite and not negative.  Of values below fp32's normal range only
-// that they are small counts.
+// The exponent e of the least 2^e with top <= most 2^e; top is finite and not
+// negative.  Of values below fp32's normal range only that they are small
+// counts.
 __device__ __forceinline__ int scale_exponent(float top, float most) {
     const uint32_t t = __float_as_uint(top), w = __float_as_uint(most);
     return (int)(t >> 23) - (int)(w >> 23) + ((t & 0x7FFFFF) > (w & 0x7FFFFF) ? 1 : 0);
 }
 
-// The distance of e4m3 values around a in [0, 448], and its inverse.
+// The distance of e4m3 values around a in [0, 448] (powers of two, from bits), and its inverse.
 __device__ __forceinline__ void grid(float a, float *step, float *inverse) {
-    const int e = max((int)(__float_as_uint(a) >> 23) - 127, -6) - 3;
-    *step = power(e);
-    *inverse = power(-e);
+    const uint32_t binade = max(__float_as_uint(a) & 0x7F800000u, 121u << 23) - (3u << 23);
+    *step = __uint_as_float(binade);
+    *inverse = __uint_as_float((254u << 23) - binade);
 }
 
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u; }
+
+// sqrt to 2 u, below the normal range too, where the instruction gives zero.
+__device__ __forceinline__ float root_of(float v) {
+    const bool small = v < 0x1p-100f;
+    return __builtin_amdgcn_sqrtf(v * (small ? 0x1p64f : 1.0f)) * (small ? 0x1p-32f : 1.0f);
+}
+
+// 1 - e^x for x <= 0, to a few u of itself: the series near 0 (what is left out
+// is below 2^-30 of it), the difference elsewhere.
+__device__ __forceinline__ float one_minus_exp(float x) {
+    float s = 1.0f / 40320.0f;
+    s = __builtin_fmaf(s, x, 1.0f / 5040.0f);
+    s = __builtin_fmaf(s, x, 1.0f / 720.0f);
+    s = __builtin_fmaf(s, x, 1.0f / 120.0f);
+    s = __builtin_fmaf(s, x, 1.0f / 24.0f);
+    s = __builtin_fmaf(s, x, 1.0f / 6.0f);
+    s = __builtin_fmaf(s, x, 0.5f);
+    s = __builtin_fmaf(s, x, 1.0f);
+    return x > -0.35f ? -x * s : 1.0f - __builtin_amdgcn_exp2f(x * 1.44269504f);
+}
+
+// Values of the type, or NaN.
+__device__ __forceinline__ uint32_t to_e4m3x4(const float (&v)[4]) {
+    const int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
+}
 
 // Eight values of a lane, each to be joined over the wave by the maximum: by
 // halves, so that ten exchanges do for the eight.  Returns the maxima of
@@ -83,13 +123,16 @@ __device__ __forceinline__ uint32_t maxima(const uint32_t (&v)[8]) {
     return c;
 }
 
+// What a step's formulas take besides the tensors.
+struct Step {
+    float scale, rate, widen, keep;         // keep: 1 - lr decay, of the tensor
+    uint32_t key;
+};
+
 template <bool E4M3, bool BF16, bool COPY>
-__device__ __forceinline__ void step_blocks(const AdamPart &part, const AdamTensor &t, uint32_t chunk) {
+__device__ __forceinline__ void step_blocks(const AdamArgs &a, const AdamTensor &t, const Step &c, uint64_t first) {
 #pragma clang fp contract(off)              // m and v round as written, wherever they are computed
-    const AdamArgs &a = part.a;
     const uint32_t lane = threadIdx.x & 63;
-    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const uint64_t first = (uint64_t)chunk * kChunk + wave * kPerWave;      // block of the tensor
     float p[kPerWave][4], g[kPerWave][4];
     f32x4 m[kPerWave], v[kPerWave];
     uint32_t mc[kPerWave], vc[kPerWave];
@@ -106,25 +149,25 @@ __device__ __forceinline__ void step_blocks(const AdamPart &part, const AdamTens
         ms[k] = vs[k] = 1.0f;
         if ((first + k) * kBlock >= t.n) continue;
         if constexpr (E4M3) {
-            mc[k] = ((const uint32_t *)a.m)[state / 4];
-            vc[k] = ((const uint32_t *)a.v)[state / 4];
+            mc[k] = __builtin_nontemporal_load((const uint32_t *)a.m + state / 4);
+            vc[k] = __builtin_nontemporal_load((const uint32_t *)a.v + state / 4);
             ms[k] = a.m_scale[t.block + first + k];
             vs[k] = a.v_scale[t.block + first + k];
         } else if (left[k]) {
-            m[k] = *(const f32x4 *)((const float *)a.m + state);
-            v[k] = *(const f32x4 *)((const float *)a.v + state);
+            m[k] = __builtin_nontemporal_load((const f32x4 *)((const float *)a.m + state));
+            v[k] = __builtin_nontemporal_load((const f32x4 *)((const float *)a.v + state));
         }
         if (left[k] == 4) {
-            const f32x4 w = ((const AnyF32x4 *)(t.p + at))->v;
+            const f32x4 w = __builtin_nontemporal_load((const AnyFloats *)(t.p + at));
 #pragma unroll
             for (int q = 0; q < 4; ++q) p[k][q] = w[q];
             if constexpr (BF16) {
-                const u32x2 h = ((const AnyU32x2 *)((const uint16_t *)t.g + at))->v;
+                const u32x2 h = __builtin_nontemporal_load((const AnyHalves *)((const uint16_t *)t.g + at));
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     g[k][q] = __uint_as_float(q & 1 ? h[q >> 1] & 0xFFFF0000u : h[q >> 1] << 16);
             } else {
-                const f32x4 h = ((const AnyF32x4 *)((const float *)t.g + at))->v;
+                const f32x4 h = __builtin_nontemporal_load((const AnyFloats *)((const float *)t.g + at));
 #pragma unroll
                 for (int q = 0; q < 4; ++q) g[k][q] = h[q];
             }
@@ -138,12 +181,7 @@ __device__ __forceinline__ void step_blocks(const AdamPart &part, const AdamTens
         }
     }
 
-    const int32_t now = *a.steps + 1;
-    const float scale = a.grad_scale ? *a.grad_scale : 1.0f, lr = a.lr_at ? *a.lr_at : a.lr;
-    // 1 - b^t without the difference of near values
-    const float c1 = -expm1f((float)now * a.log_b1), c2 = -expm1f((float)now * a.log_b2);
-    const float rate = lr / c1, widen = 1.0f / sqrtf(c2), keep = 1.0f - lr * t.decay;
-    uint32_t top[8] = {};                   // of |m| and of v, the finite ones
+    uint32_t top[8] = {};                   // of |m| and of v; what is past the tensor's end is zero
 #pragma unroll
     for (int k = 0; k < kPerWave; ++k) {
         if constexpr (E4M3) {
@@ -158,32 +196,45 @@ __device__ __forceinline__ void step_blocks(const AdamPart &part, const AdamTens
                 v[k][q] = root * root;
             }
         }
+        float most[2] = {0.0f, 0.0f};       // without NaN
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float d = g[k][q] * scale;
+            const float d = g[k][q] * c.scale;
             m[k][q] = m[k][q] * a.b1 + d * a.rest1;
             v[k][q] = v[k][q] * a.b2 + (d * d) * a.rest2;
-            p[k][q] = p[k][q] * keep - rate * m[k][q] / (sqrtf(v[k][q]) * widen + a.eps);
-            if constexpr (E4M3) {
-                if (q < left[k]) {
+            const float below = root_of(v[k][q]) * c.widen + a.eps;
+            p[k][q] = p[k][q] * c.keep - c.rate * m[k][q] * __builtin_amdgcn_rcpf(below);
+            most[0] = fmaxf(most[0], fabsf(m[k][q]));
+            most[1] = fmaxf(most[1], v[k][q]);
+        }
+        top[k] = __float_as_uint(most[0]);
+        top[kPerWave + k] = __float_as_uint(most[1]);
+    }
+    uint32_t all = 0;
+    bool infinite = false;
+    if constexpr (E4M3) {
+        static_assert(kPerWave == 4, "eight maxima");
+        all = maxima(top);
+        if (__ballot(all == 0x7F800000u)) { // seldom: the largest of those that are finite
+            infinite = true;
+#pragma unroll
+            for (int k = 0; k < kPerWave; ++k) {
+                top[k] = top[kPerWave + k] = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
                     if (finite(m[k][q])) top[k] = max(top[k], __float_as_uint(fabsf(m[k][q])));
                     if (finite(v[k][q])) top[kPerWave + k] = max(top[kPerWave + k], __float_as_uint(v[k][q]));
                 }
             }
+            all = maxima(top);
         }
-    }
-    uint32_t all = 0, key = 0;
-    if constexpr (E4M3) {
-        static_assert(kPerWave == 4, "eight maxima");
-        all = maxima(top);
-        key = mix((uint32_t)now ^ mix(a.seed));
     }
 #pragma unroll
     for (int k = 0; k < kPerWave; ++k) {
         if ((first + k) * kBlock >= t.n) continue;
         const uint64_t at = (first + k) * kBlock + lane * 4, state = t.block * kBlock + at;
         if (left[k] == 4) {
-            ((AnyF32x4 *)(t.p + at))->v = f32x4{p[k][0], p[k][1], p[k][2], p[k][3]};
+            __builtin_nontemporal_store((AnyFloats){p[k][0], p[k][1], p[k][2], p[k][3]}, (AnyFloats *)(t.p + at));
             if constexpr (COPY)
                 ((AnyU32x2 *)(t.copy + at))->v = u32x2{f32_to_bf16x2(p[k][0], p[k][1]), f32_to_bf16x2(p[k][2], p[k][3])};
         } else {
@@ -197,8 +248,8 @@ __device__ __forceinline__ void step_blocks(const AdamPart &part, const AdamTens
         if constexpr (!E4M3) {
             // past the tensor's end a block holds zeros: their values stay
             if (left[k]) {
-                *(f32x4 *)((float *)a.m + state) = m[k];
-                *(f32x4 *)((float *)a.v + state) = v[k];
+                __builtin_nontemporal_store(m[k], (f32x4 *)((float *)a.m + state));
+                __builtin_nontemporal_store(v[k], (f32x4 *)((float *)a.v + state));
             }
         } else {
             const float m_top = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)all, k * 8));
@@ -206,7 +257,7 @@ __device__ __forceinline__ void step_blocks(const AdamPart &part, const AdamTens
             const int em = max(scale_exponent(m_top, 448.0f), kLeastScale);
             const int e2 = scale_exponent(v_top, kRootMax), ev = max((e2 + (e2 & 1)) / 2, kLeastScale);
             const float m_inverse = power(-em), v_inverse = power(-2 * ev);
-            const uint32_t base = mix((uint32_t)(state >> 32) ^ key);
+            const uint32_t base = mix((uint32_t)(state >> 32) ^ c.key);
             float mq[4], vq[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -215,18 +266,22 @@ __device__ __forceinline__ void step_blocks(const AdamPart &part, const AdamTens
                 float step, inverse;
                 const float x = fabsf(m[k][q]) * m_inverse;
                 grid(x, &step, &inverse);
-                mq[q] = __builtin_copysignf(floorf(x * inverse + um) * step, m[k][q]);
-                const float b = v[k][q] * v_inverse, root = sqrtf(b);
+                // the product is exact, a step being a power of two
+                mq[q] = __builtin_copysignf(floorf(__builtin_fmaf(x, inverse, um)) * step, m[k][q]);
+                // A root next to a value of the grid may fall on either side of
+                // it: the comparison with v itself then leads to that value.
+                const float b = v[k][q] * v_inverse, root = __builtin_amdgcn_sqrtf(b);
                 grid(root, &step, &inverse);
                 const float low = floorf(root * inverse);
-                const float up = uv * (2.0f * low + 1.0f) < b * inverse * inverse - low * low ? 1.0f : 0.0f;
-                vq[q] = (low + up) * step;
-                if (!finite(m[k][q])) mq[q] = __builtin_nanf("");
-                if (!finite(v[k][q])) vq[q] = __builtin_nanf("");
-                if (q >= left[k]) mq[q] = vq[q] = 0.0f;
+                const bool up = uv * __builtin_fmaf(2.0f, low, 1.0f) < __builtin_fmaf(-low, low, b * (inverse * inverse));
+                vq[q] = (up ? low + 1.0f : low) * step;
+                if (infinite) {
+                    if (!finite(m[k][q])) mq[q] = __builtin_nanf("");
+                    if (!finite(v[k][q])) vq[q] = __builtin_nanf("");
+                }
             }
-            ((uint32_t *)a.m)[state / 4] = f32_to_e4m3x4(mq[0], mq[1], mq[2], mq[3]);
-            ((uint32_t *)a.v)[state / 4] = f32_to_e4m3x4(vq[0], vq[1], vq[2], vq[3]);
+            __builtin_nontemporal_store(to_e4m3x4(mq), (uint32_t *)a.m + state / 4);
+            __builtin_nontemporal_store(to_e4m3x4(vq), (uint32_t *)a.v + state / 4);
             if (lane == 0) {
                 a.m_scale[t.block + first + k] = power(em);
                 a.v_scale[t.block + first + k] = power(ev);
@@ -235,62 +290,90 @@ __device__ __forceinline__ void step_blocks(const AdamPart &part, const AdamTens
     }
 }
 
-template <bool E4M3>
-__global__ __launch_bounds__(kWaves * 64) void adamw_kernel(AdamPart part) {
-    // the tensor of this workgroup: the last that begins at or before it
+// A wave takes kPerWave blocks of a tensor at a time, the waves of the launch
+// one after the other.  ALONE: the launch is one workgroup, which moves the
+// step's number on itself.
+template <bool E4M3, int WAVES, bool ALONE>
+__global__ __launch_bounds__(WAVES * 64) void adamw_kernel(AdamPart part) {
+    const AdamArgs &a = part.a;
     const uint32_t lane = threadIdx.x & 63;
-    const uint64_t mask = __ballot(lane < part.count && part.first[lane] <= blockIdx.x);
-    const uint32_t k = (uint32_t)__builtin_amdgcn_readfirstlane(63 - __clzll((long long)mask));
-    const AdamTensor &t = part.t[k];
-    const uint32_t chunk = blockIdx.x - part.first[k];
-    if (t.grad_bf16)
-        t.copy ? step_blocks<E4M3, true, true>(part, t, chunk) : step_blocks<E4M3, true, false>(part, t, chunk);
-    else
-        t.copy ? step_blocks<E4M3, false, true>(part, t, chunk) : step_blocks<E4M3, false, false>(part, t, chunk);
+    const int32_t now = *a.steps + 1;
+    Step c;
+    c.scale = a.grad_scale ? *a.grad_scale : 1.0f;
+    const float lr = a.lr_at ? *a.lr_at : a.lr;
+    c.rate = lr / one_minus_exp((float)now * a.log_b1);
+    c.widen = 1.0f / sqrtf(one_minus_exp((float)now * a.log_b2));
+    c.key = mix((uint32_t)now ^ mix(a.seed));
+    if constexpr (ALONE) {
+        __syncthreads();                    // every wave has the number
+        if (threadIdx.x == 0) *a.steps = now;
+    }
+    const uint32_t begins = lane < part.count ? part.first[lane] : 0xFFFFFFFFu;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    for (uint32_t i = blockIdx.x * WAVES + wave; i < part.chunks; i += gridDim.x * WAVES) {
+        // the last tensor that begins at or before i
+        const uint32_t k = (uint32_t)__builtin_amdgcn_readfirstlane(63 - __clzll((long long)__ballot(begins <= i)));
+        const AdamTensor &t = part.t[k];
+        const uint64_t first = (uint64_t)(i - part.first[k]) * kPerWave;
+        c.keep = 1.0f - lr * t.decay;
+        if (t.grad_bf16)
+            t.copy ? step_blocks<E4M3, true, true>(a, t, c, first) : step_blocks<E4M3, true, false>(a, t, c, first);
+        else
+            t.copy ? step_blocks<E4M3, false, true>(a, t, c, first) : step_blocks<E4M3, false, false>(a, t, c, first);
+    }
 }
 
 __global__ void advance_kernel(int32_t *steps) { *steps += 1; }
+
+template <bool E4M3>
+void launch_part(const AdamPart &part, bool alone, hipStream_t s) {
+    if (alone)
+        adamw_kernel<E4M3, kAloneWaves, true><<<1, kAloneWaves * 64, 0, s>>>(part);
+    else {
+        const uint32_t need = (part.chunks + kWaves - 1) / kWaves;
+        adamw_kernel<E4M3, kWaves, false><<<need < kMostBlocks ? need : kMostBlocks, kWaves * 64, 0, s>>>(part);
+    }
+}
 
 }  // namespace
 
 uint64_t adamw_blocks(uint64_t n) { return (n + kBlock - 1) / kBlock; }
 
-hipError_t AdamBatch::launch() {
+hipError_t AdamBatch::launch(bool alone) {
     if (!part.count) return hipSuccess;
-    if (part.a.e4m3)
-        adamw_kernel<true><<<part.blocks, kWaves * 64, 0, stream>>>(part);
-    else
-        adamw_kernel<false><<<part.blocks, kWaves * 64, 0, stream>>>(part);
-    part.count = part.blocks = 0;
+    part.a.e4m3 ? launch_part<true>(part, alone, stream) : launch_part<false>(part, alone, stream);
+    launched = true;
+    part.count = part.chunks = 0;
     return hipGetLastError();
 }
 
 hipError_t AdamBatch::add(AdamTensor t) {
-    constexpr uint32_t kMost = 1u << 22;    // workgroups a launch: 2^30 threads
-    while (t.n) {                           // a tensor of more than a launch's workgroups is cut at a block
-        if (part.count == kAdamTensors || part.blocks == kMost) {
-            const hipError_t e = launch();
+    constexpr uint32_t kMost = 1u << 31;    // chunks a launch
+    while (t.n) {                           // a tensor of more than a launch's chunks is cut at a block
+        if (part.count == kAdamTensors || part.chunks == kMost) {
+            const hipError_t e = launch(false);
             if (e != hipSuccess) return e;
         }
-        const uint64_t chunks = (adamw_blocks(t.n) + kChunk - 1) / kChunk, room = kMost - part.blocks;
-        const uint64_t now = chunks < room ? chunks : room, values = now * kChunk * kBlock;
+        const uint64_t chunks = (adamw_blocks(t.n) + kPerWave - 1) / kPerWave, room = kMost - part.chunks;
+        const uint64_t now = chunks < room ? chunks : room, values = now * kPerWave * kBlock;
         AdamTensor &to = part.t[part.count];
         to = t;
         if (to.n > values) to.n = values;
-        part.first[part.count++] = part.blocks;
-        part.blocks += (uint32_t)now;
+        part.first[part.count++] = part.chunks;
+        part.chunks += (uint32_t)now;
         t.p += to.n;
         t.g = (const char *)t.g + to.n * (t.grad_bf16 ? 2 : 4);
         if (t.copy) t.copy += to.n;
-        t.block += now * kChunk;
+        t.block += now * kPerWave;
         t.n -= to.n;
     }
     return hipSuccess;
 }
 
 hipError_t AdamBatch::finish() {
-    const hipError_t e = launch();
-    if (e != hipSuccess) return e;
+    const bool alone = !launched && part.count && part.chunks <= kAloneChunks;
+    const hipError_t e = launch(alone);
+    if (e != hipSuccess || alone) return e;
     advance_kernel<<<1, 1, 0, stream>>>(part.a.steps);
     return hipGetLastError();
 }

@@ -29,8 +29,8 @@ struct AdamArgs {
 
 struct AdamPart {                           // of a launch
     AdamTensor t[kAdamTensors];
-    uint32_t first[kAdamTensors];           // workgroup
-    uint32_t count, blocks;
+    uint32_t first[kAdamTensors];           // chunk
+    uint32_t count, chunks;
     AdamArgs a;
 };
 static_assert(sizeof(AdamPart) <= 4096, "kernel arguments");
@@ -39,13 +39,14 @@ static_assert(sizeof(AdamPart) <= 4096, "kernel arguments");
 struct AdamBatch {
     AdamPart part;
     hipStream_t stream;
+    bool launched = false;
 
     AdamBatch(const AdamArgs &a, hipStream_t s) : stream(s) {
         part.a = a;
-        part.count = part.blocks = 0;
+        part.count = part.chunks = 0;
     }
     hipError_t add(AdamTensor t);
-    hipError_t launch();
+    hipError_t launch(bool alone);           // alone: the only launch of the step
     hipError_t finish();                    // the last launch, and the step's number
 };
 

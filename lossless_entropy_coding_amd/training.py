@@ -10,13 +10,15 @@ on the GPU, so that the calls can be captured into a HIP graph and replayed.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import math
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
-from .ffn import (_BF16, _DTYPES, _E4M3, _FP32, _ec, _empty, _error, _given, _matrix, _placed, _row_stride, _run, _status,
+from .ffn import (_BF16, _DTYPES, _E4M3, _FP32, _current_device, _ec, _empty, _error, _given, _matrix, _placed, _row_stride, _run, _status,
                   _vector, _warn_unrecorded)
 
 _vp, _u64, _u32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32
@@ -194,11 +196,23 @@ def adamw_state(params, state_dtype=torch.float32) -> AdamWState:
     return AdamWState(zeros(), zeros(), ones(), ones(), torch.zeros(1, dtype=torch.int32, device=dev))
 
 
-def _number(v, name: str, least, below=None) -> float:
+def _number(v, name: str, least, below=math.inf) -> float:
     v = float(v)
-    if not (v >= least and math.isfinite(v)) or (below is not None and v >= below):
-        _error("%s must be %s, not %r" % (name, "at least %g" % least if below is None else "in [%g, %g)" % (least, below), v))
+    if not least <= v < below:
+        _error("%s must be %s, not %r" % (name, "at least %g" % least if below == math.inf else "in [%g, %g)" % (least, below), v))
     return v
+
+
+_STATES = (torch.float32, torch.float8_e4m3fn, torch.uint8)
+
+
+def _float_bits(v: float) -> int:
+    return struct.unpack("<I", struct.pack("<f", v))[0]
+
+
+def _bad_param(p, dev):
+    _params([p])
+    _error("params are on %s and %s" % (dev, p.device))
 
 
 def adamw(params, grads, state: AdamWState, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=None,
@@ -207,8 +221,8 @@ def adamw(params, grads, state: AdamWState, *, lr=1e-3, betas=(0.9, 0.999), eps=
     place.
 
     params: contiguous float32 tensors of any shapes on one device; grads: one
-    for each, of its shape, bfloat16 or float32 (as the backward functions
-    give them); state: ``adamw_state(params)``, updated in place, its step
+    for each, contiguous, of as many values, bfloat16 or float32 (as the
+    backward functions give them); state: ``adamw_state(params)``, updated in place, its step
     number too.  lr a number, or a float32 [1] tensor read on the GPU;
     weight_decay a number or one for each tensor; grad_scale float32 [1]
     multiplies the gradients (what clipping their norm gives).  copies:
@@ -219,81 +233,76 @@ def adamw(params, grads, state: AdamWState, *, lr=1e-3, betas=(0.9, 0.999), eps=
     kept: by a function of seed (32 bits), the step's number and the place, so
     that the same call gives the same bits.  Values that are not finite become
     NaN there.  No two tensors may overlap."""
-    if stream is not None:
-        if params and isinstance(params[0], torch.Tensor) and params[0].is_cuda and stream.device != params[0].device:
-            _error("stream is on %s, params on %s" % (stream.device, params[0].device))
-        with torch.cuda.stream(stream):
-            return adamw(params, grads, state, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
-                         grad_scale=grad_scale, copies=copies, seed=seed)
-    _params(params)
-    dev, count = params[0].device, len(params)
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return adamw(params, grads, state, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
-                         grad_scale=grad_scale, copies=copies, seed=seed)
-    for t, name in ((grads, "grads"), (copies, "copies")):
-        if t is None and name == "copies":
-            continue
-        if not isinstance(t, (list, tuple)) or len(t) != count:
-            _error("%s must be a list or tuple of %d, one for each of params" % (name, count))
-    a = _AdamWArgs()
-    decays = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
-    if len(decays) != count:
-        _error("weight_decay must be a number or one for each of params (%d)" % count)
-    if not isinstance(weight_decay, (list, tuple)):
-        _number(weight_decay, "weight_decay", 0.0)
+    if not isinstance(params, (list, tuple)) or not params or not isinstance(params[0], torch.Tensor) or not params[0].is_cuda:
+        _params(params)
+    if stream is not None and stream.device != params[0].device:
+        _error("stream is on %s, params on %s" % (stream.device, params[0].device))
+    index = params[0].get_device()
+    if stream is not None or index != _current_device():
+        with torch.cuda.stream(stream), torch.cuda.device(index):
+            return adamw(params, grads, state, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, grad_scale=grad_scale,
+                         copies=copies, seed=seed)
+    count, dev = len(params), params[0].device
+    if not isinstance(grads, (list, tuple)) or len(grads) != count:
+        _error("grads must be a list or tuple of %d, one for each of params" % count)
+    if copies is not None and (not isinstance(copies, (list, tuple)) or len(copies) != count):
+        _error("copies must be a list or tuple of %d, one for each of params" % count)
+    if isinstance(weight_decay, (list, tuple)):
+        if len(weight_decay) != count:
+            _error("weight_decay must be a number or one for each of params (%d)" % count)
+        decays = [_float_bits(_number(d, "weight_decay", 0.0, 1e38)) << 32 for d in weight_decay]
     else:
-        for d in decays:
-            _number(d, "weight_decay", 0.0)
-    tensors = (_AdamWTensor * count)()
-    blocks = 0
-    for i, p in enumerate(params):
-        g, t = grads[i], tensors[i]
-        if p.device != dev:
-            _error("params are on %s and %s" % (dev, p.device))
+        decays = [_float_bits(_number(weight_decay, "weight_decay", 0.0, 1e38)) << 32] * count
+    # one pass of cheap checks: a step of small tensors takes as long as the host needs for it
+    words, blocks = [], 0                       # ec_adamw_tensor's, five of 64 bits
+    fp32, bf16, Tensor = torch.float32, torch.bfloat16, torch.Tensor
+    for p, g, c, decay in zip(params, grads, copies if copies is not None else [None] * count, decays):
+        if not (isinstance(p, Tensor) and p.dtype is fp32 and p.get_device() == index and p.is_contiguous()):
+            _bad_param(p, dev)
         n = p.numel()
-        if not isinstance(g, torch.Tensor) or g.shape != p.shape or g.device != dev or not g.is_contiguous():
-            _error("grads[%d] must be a contiguous tensor of %s on %s" % (i, list(p.shape), dev))
-        if g.dtype == torch.bfloat16:
-            t.grad_dtype = _BF16
-        elif g.dtype == torch.float32:
-            t.grad_dtype = _FP32
+        if not (isinstance(g, Tensor) and g.get_device() == index and g.numel() == n and g.is_contiguous()):
+            _error("grads must be contiguous tensors on %s of as many values as params" % dev)
+        kind = g.dtype
+        if kind is bf16:
+            decay |= _BF16
+        elif kind is fp32:
+            decay |= _FP32
         else:
-            _error("grads[%d] must be bfloat16 or float32, not %s" % (i, g.dtype))
-        t.param, t.grad, t.n, t.weight_decay = p.data_ptr(), g.data_ptr(), n, decays[i]
-        c = copies[i] if copies is not None else None
+            _error("grads must be bfloat16 or float32, not %s" % kind)
+        copy = 0
         if c is not None:
-            if (not isinstance(c, torch.Tensor) or c.dtype != torch.bfloat16 or c.shape != p.shape or c.device != dev
-                    or not c.is_contiguous()):
-                _error("copies[%d] must be a contiguous bfloat16 tensor of %s on %s" % (i, list(p.shape), dev))
-            t.copy = c.data_ptr()
-        blocks += -(-n // ADAMW_BLOCK)
+            if not (isinstance(c, Tensor) and c.dtype is bf16 and c.get_device() == index and c.numel() == n
+                    and c.is_contiguous()):
+                _error("copies must be contiguous bfloat16 tensors on %s of as many values as params, or None" % dev)
+            copy = c.data_ptr()
+        words += (p.data_ptr(), g.data_ptr(), copy, n, decay)
+        blocks += (n + 255) >> 8
     m, v, m_scale, v_scale, steps = state
-    kinds = (torch.float32, torch.float8_e4m3fn, torch.uint8)
     length = ((blocks * ADAMW_BLOCK,),)
-    _vector(m, "state.m", length, kinds, dev)
-    _vector(v, "state.v", length, kinds, dev)
-    a.state_dtype = _DTYPES[m.dtype]
-    if _DTYPES[v.dtype] != a.state_dtype:
+    _vector(m, "state.m", length, _STATES, dev)
+    _vector(v, "state.v", length, _STATES, dev)
+    kind = _DTYPES[m.dtype]
+    if _DTYPES[v.dtype] != kind:
         _error("state.m is %s, state.v %s" % (m.dtype, v.dtype))
-    if a.state_dtype == _E4M3:
-        _vector(m_scale, "state.m_scale", ((blocks,),), (torch.float32,), dev)
-        _vector(v_scale, "state.v_scale", ((blocks,),), (torch.float32,), dev)
-        a.m_scale, a.v_scale = m_scale.data_ptr(), v_scale.data_ptr()
+    scales = (None, None)
+    if kind == _E4M3:
+        _vector(m_scale, "state.m_scale", ((blocks,),), (fp32,), dev)
+        _vector(v_scale, "state.v_scale", ((blocks,),), (fp32,), dev)
+        scales = m_scale.data_ptr(), v_scale.data_ptr()
     _vector(steps, "state.steps", ((1,),), (torch.int32,), dev)
-    a.m, a.v, a.steps, a.state_blocks = m.data_ptr(), v.data_ptr(), steps.data_ptr(), blocks
-    if isinstance(lr, torch.Tensor):
-        _vector(lr, "lr", ((1,),), (torch.float32,), dev)
-        a.lr_at = lr.data_ptr()
-    else:
-        a.lr = _number(lr, "lr", 0.0)
+    lr_at = None
+    if isinstance(lr, Tensor):
+        _vector(lr, "lr", ((1,),), (fp32,), dev)
+        lr, lr_at = 0.0, lr.data_ptr()
     if grad_scale is not None:
-        _vector(grad_scale, "grad_scale", ((1,),), (torch.float32,), dev)
-        a.grad_scale = grad_scale.data_ptr()
-    a.beta1, a.beta2 = _number(betas[0], "betas[0]", 0.0, 1.0), _number(betas[1], "betas[1]", 0.0, 1.0)
-    a.eps = _number(eps, "eps", 0.0)
+        _vector(grad_scale, "grad_scale", ((1,),), (fp32,), dev)
+        grad_scale = grad_scale.data_ptr()
     if not isinstance(seed, int) or not 0 <= seed < 1 << 32:
         _error("seed must be a whole number of 32 bits, not %r" % (seed,))
-    a.seed = seed
+    beta1, beta2 = betas
+    a = _AdamWArgs(m.data_ptr(), v.data_ptr(), *scales, blocks, steps.data_ptr(), lr_at, grad_scale, _number(lr, "lr", 0.0),
+                   _number(beta1, "betas[0]", 0.0, 1.0), _number(beta2, "betas[1]", 0.0, 1.0), _number(eps, "eps", 0.0), kind,
+                   seed)
     ec = _ec()
-    ec._check(ec.lib().adamw_step(tensors, count, ctypes.byref(a), ec._stream(None)), "adamw_step")
+    tensors = array.array("Q", words)
+    ec._check(ec.lib().adamw_step(tensors.buffer_info()[0], count, ctypes.byref(a), ec._stream(None)), "adamw_step")
