@@ -404,10 +404,9 @@ GatedGrad gated_grad(const ec_linear_args *a, void *workspace) {
     g.dz = (uint16_t *)ws;
     g.pitch = (2 * a->n + 7) / 8 * 8;
     g.db = a->d_db;
-    const uint32_t parts = gated_grad_parts(g);
+    g.slab = gated_grad_slab(g.m, g.n);
     q.partial = (a->m * g.pitch * 2 + 255) / 256 * 256;
-    q.product = q.partial;
-    if (a->d_db && parts > 1) q.product += ((uint64_t)parts * (a->groups ? a->groups : 1) * 2 * a->n * 4 + 255) / 256 * 256;
+    q.product = q.partial + (gated_grad_workspace(g) + 255) / 256 * 256;
     g.partial = (float *)(ws + q.partial);
     q.bytes = q.product;
     // the products of dz, as of the gradient of a product with 2 n columns

@@ -99,7 +99,6 @@ hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s);
 hipError_t launch_check_offsets(const int32_t *offsets, uint32_t groups, uint32_t m, uint32_t *status, hipStream_t s);
 uint64_t column_sum_workspace(const ColumnSumArgs &a);
 hipError_t launch_column_sum(const ColumnSumArgs &a, float *workspace, hipStream_t s);
-hipError_t launch_column_join(const float *in, float *out, uint64_t n, uint32_t parts, hipStream_t s);
 hipError_t launch_copy_rows(const void *in, uint64_t stride, uint64_t rows, uint64_t cols, uint32_t dtype, void *out,
                             uint64_t pitch, hipStream_t s);
 
@@ -114,11 +113,13 @@ struct GatedGradArgs {
     uint16_t *dz;                          // [m, pitch], zeros in columns 2 n ..; rows of no group are left as they are
     uint64_t pitch;
     float *db;                             // [groups][2 n], or null
-    float *partial;                        // [parts][groups][2 n] when parts > 1
+    uint32_t slab;                         // rows a workgroup takes
+    float *partial;                        // [slabs + groups][2 n]
 };
 
 hipError_t launch_gated(ProductArgs a, void *workspace, hipStream_t s);
-uint32_t gated_grad_parts(const GatedGradArgs &a);
+uint32_t gated_grad_slab(uint32_t m, uint32_t n);
+uint64_t gated_grad_workspace(const GatedGradArgs &a);
 hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s);
 
 // Cross entropy over the products of x and w, forward and backward.

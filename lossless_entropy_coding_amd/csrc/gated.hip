@@ -8,53 +8,64 @@ namespace {
 // ------------------------------------------------------------------ few rows
 //
 // As few_rows_kernel, with the 16 columns' rows of the gate and of the factor
-// beside it: twice the loads of B on each of A.
-template <int RT, int ACT>
-__device__ __forceinline__ void few_gated_finish(const ProductArgs &p, const Place &q, const float *sums, uint32_t waves) {
-    const uint32_t t = threadIdx.x, i = q.i0 + (t >> 1), j = q.j0 + (t & 1) * 8;
-    if (t >= RT * 32 || i >= q.i1) return;
-    const GatedColumns c = load_gated_columns(p, q.group, j);
-    const float xs = p.x_scale ? p.x_scale[p.x_scales > 1 ? i : 0] : 1.0f, os = p.out_scale ? *p.out_scale : 1.0f;
-    float gate[8] = {}, rest[8] = {};
-    few_sums<RT>(sums, waves, gate);
-    few_sums<RT>(sums + waves * RT * 16 * 20, waves, rest);
-    finish8_gated<ACT>(p, i, j, gate, rest, c, xs, os, q.zero);
-}
+// beside it.  A wave takes both, or (SPLIT) half of the waves one and half the
+// other: then a lane has eight loads of one stretch of memory on the way and
+// not four of each of two.  One row by 2 x 16384 x 2048 bf16 weights: 28.5 us
+// split over eight waves (4.7 TB/s), 31.4 over four, 33.8 not split.  Where
+// workgroups are few or have more rows the loads of A weigh more: 4 rows by 2 x
+// 2048 x 8192 26 us split, 22.9 not; 16 by 2 x 8192 x 2048 19.6 and 17.6; 17 by
+// 2 x 16384 x 2048 46 and 42; 64 rows over 32 experts of 2 x 1024 x 2048 in
+// e4m3 34 and 28.8.
+constexpr uint32_t kSplitBlocks = 512, kSplitRows = 4;
 
 template <int RT>
 struct FewGated {
     static constexpr int TI = RT * 16, TJ = 32;         // TJ: rows of B, for 16 columns
 };
 
-template <int RT, int W, bool E4M3>
+template <int RT, int ACT>
+__device__ __forceinline__ void few_gated_finish(const ProductArgs &p, const Place &q, const float *sums, uint32_t parts) {
+    const uint32_t t = threadIdx.x, i = q.i0 + (t >> 1), j = q.j0 + (t & 1) * 8;
+    if (t >= RT * 32 || i >= q.i1) return;
+    const GatedColumns c = load_gated_columns(p, q.group, j);
+    const float xs = p.x_scale ? p.x_scale[p.x_scales > 1 ? i : 0] : 1.0f, os = p.out_scale ? *p.out_scale : 1.0f;
+    float gate[8] = {}, rest[8] = {};
+    few_sums<RT>(sums, parts, gate);
+    few_sums<RT>(sums + parts * RT * 16 * 20, parts, rest);
+    finish8_gated<ACT>(p, i, j, gate, rest, c, xs, os, q.zero);
+}
+
+template <int RT, int W, bool E4M3, bool SPLIT>
 __global__ __launch_bounds__(W * 64) void few_gated_kernel(ProductArgs p) {
-    constexpr int ES = E4M3 ? 1 : 2, U = 4;             // steps whose loads are on the way in a lane
+    // halves a wave takes, parts of the contraction, steps whose loads are on the way
+    constexpr int ES = E4M3 ? 1 : 2, H = SPLIT ? 1 : 2, P = SPLIT ? W / 2 : W, U = 8 / H;
     using T = FewGated<RT>;
-    __shared__ __attribute__((aligned(16))) float sums[2 * W * RT * 16 * 20];   // [half][wave][row][16 columns and a gap]
+    __shared__ __attribute__((aligned(16))) float sums[2 * P * RT * 16 * 20];   // [half][part][row][16 columns and a gap]
     if (p.groups && blockIdx.x == 0 && threadIdx.x < 64) check_offsets(p.offsets, p.groups, p.I, p.status);
     const Place q = find_place<T, kOpGated>(p, blockIdx.x);
     if (q.none) return;
-    const uint32_t lane = threadIdx.x & 63, row = lane & 15, part = (lane >> 4) * 16;
+    const uint32_t lane = threadIdx.x & 63, row = lane & 15, chunk = (lane >> 4) * 16;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t half = wave / P, part = wave % P;
     // rows and columns that do not exist repeat the last one: their sums are not stored
-    const uint64_t column = min(q.j0 + row, p.J - 1);
-    const char *b[2], *a[RT];
+    const uint64_t column = min(q.j0 + row, p.J - 1) + (uint64_t)half * p.J;
+    const char *b[H], *a[RT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        b[h] = (const char *)p.b + (q.group * p.b_group + (column + (h ? p.J : 0)) * p.b_j) * ES + part;
+    for (int h = 0; h < H; ++h)
+        b[h] = (const char *)p.b + (q.group * p.b_group + (column + (uint64_t)h * p.J) * p.b_j) * ES + chunk;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) a[t] = (const char *)p.a + min(q.i0 + t * 16 + row, q.i1 - 1) * p.a_i * ES + part;
+    for (int t = 0; t < RT; ++t) a[t] = (const char *)p.a + min(q.i0 + t * 16 + row, q.i1 - 1) * p.a_i * ES + chunk;
     const uint64_t bytes = (uint64_t)(q.c1 - q.c0) * ES;
     const uint32_t steps = (uint32_t)((bytes + 63) / 64), whole = (uint32_t)(bytes / 64);
-    uint32_t s = (uint32_t)((uint64_t)steps * wave / W);
-    const uint32_t s1 = (uint32_t)((uint64_t)steps * (wave + 1) / W);
-    f32x4 acc[2][RT] = {};
+    uint32_t s = (uint32_t)((uint64_t)steps * part / P);
+    const uint32_t s1 = (uint32_t)((uint64_t)steps * (part + 1) / P);
+    f32x4 acc[H][RT] = {};
     for (; s + U <= min(s1, whole); s += U) {
-        u32x4 vb[U][2], va[U][RT];
+        u32x4 vb[U][H], va[U][RT];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) vb[u][h] = ((const AnyByteU32x4 *)(b[h] + (uint64_t)(s + u) * 64))->v;
+            for (int h = 0; h < H; ++h) vb[u][h] = ((const AnyByteU32x4 *)(b[h] + (uint64_t)(s + u) * 64))->v;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -62,45 +73,50 @@ __global__ __launch_bounds__(W * 64) void few_gated_kernel(ProductArgs p) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) few_multiply<RT, E4M3>(acc[h], vb[u][h], va[u]);
+            for (int h = 0; h < H; ++h) few_multiply<RT, E4M3>(acc[h], vb[u][h], va[u]);
     }
     for (; s < s1; ++s) {
-        u32x4 vb[2] = {}, va[RT] = {};
-        const uint64_t at = (uint64_t)s * 64 + part;
+        u32x4 vb[H] = {}, va[RT] = {};
+        const uint64_t at = (uint64_t)s * 64 + chunk;
         if (at < bytes) {
             const uint32_t n = (uint32_t)min(bytes - at, (uint64_t)16) / ES;    // 16 / ES, or the row's last values
             const auto value = [&](const char *from) {
                 return n == 16 / ES ? ((const AnyByteU32x4 *)from)->v : few_values<ES>(from, n);
             };
 #pragma unroll
-            for (int h = 0; h < 2; ++h) vb[h] = value(b[h] + (uint64_t)s * 64);
+            for (int h = 0; h < H; ++h) vb[h] = value(b[h] + (uint64_t)s * 64);
 #pragma unroll
             for (int t = 0; t < RT; ++t) va[t] = value(a[t] + (uint64_t)s * 64);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) few_multiply<RT, E4M3>(acc[h], vb[h], va);
+        for (int h = 0; h < H; ++h) few_multiply<RT, E4M3>(acc[h], vb[h], va);
     }
     // the accumulators hold row lane % 16, columns 4 (lane / 16) + r
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-            *(f32x4 *)(sums + ((h * W + wave) * (RT * 16) + t * 16 + row) * 20 + (lane >> 4) * 4) = acc[h][t];
+            *(f32x4 *)(sums + (((half + h) * P + part) * (RT * 16) + t * 16 + row) * 20 + (lane >> 4) * 4) = acc[h][t];
     __syncthreads();
     switch (p.act) {
-        case EC_ACT_GELU: few_gated_finish<RT, EC_ACT_GELU>(p, q, sums, W); break;
-        case EC_ACT_SILU: few_gated_finish<RT, EC_ACT_SILU>(p, q, sums, W); break;
-        case EC_ACT_RELU: few_gated_finish<RT, EC_ACT_RELU>(p, q, sums, W); break;
-        default: few_gated_finish<RT, EC_ACT_NONE>(p, q, sums, W);
+        case EC_ACT_GELU: few_gated_finish<RT, EC_ACT_GELU>(p, q, sums, P); break;
+        case EC_ACT_SILU: few_gated_finish<RT, EC_ACT_SILU>(p, q, sums, P); break;
+        case EC_ACT_RELU: few_gated_finish<RT, EC_ACT_RELU>(p, q, sums, P); break;
+        default: few_gated_finish<RT, EC_ACT_NONE>(p, q, sums, P);
     }
 }
 
-template <int RT, bool E4M3>
+template <bool E4M3>
 void launch_few(const ProductArgs &a, const Plan &q, hipStream_t s) {
-    if (q.waves == 4)
-        few_gated_kernel<RT, 4, E4M3><<<(uint32_t)q.blocks, 256, 0, s>>>(a);
+    const uint32_t n = (uint32_t)q.blocks;
+    if (q.row_tiles == 2)
+        q.waves == 4 ? few_gated_kernel<2, 4, E4M3, false><<<n, 256, 0, s>>>(a)
+                     : few_gated_kernel<2, 8, E4M3, false><<<n, 512, 0, s>>>(a);
+    else if (!a.groups && a.I <= kSplitRows && n >= kSplitBlocks)
+        few_gated_kernel<1, 8, E4M3, true><<<n, 512, 0, s>>>(a);
     else
-        few_gated_kernel<RT, 8, E4M3><<<(uint32_t)q.blocks, 512, 0, s>>>(a);
+        q.waves == 4 ? few_gated_kernel<1, 4, E4M3, false><<<n, 256, 0, s>>>(a)
+                     : few_gated_kernel<1, 8, E4M3, false><<<n, 512, 0, s>>>(a);
 }
 
 template <class T>
@@ -116,46 +132,48 @@ void launch_tiles(const ProductArgs &a, const Plan &q, hipStream_t s) {
 //
 // dz = [dy rest act'(gate), dy act(gate)], rounded to bf16 for the matrix units
 // of the products that follow, and the sums of its rows before the rounding.
-// A workgroup takes 128 columns of both halves in one part of a group's rows,
-// 16 threads of eight columns by 16 rows.  Bound by HBM: 10 bytes a value of
-// dy, one pass over each.
+// A workgroup takes 128 columns of both halves in a slab of rows, 16 threads of
+// eight columns by 16 rows; by group it takes the runs of groups in its slab
+// one after the other.  The sums of slab s's run of group g are part s + g,
+// which no other run has, and a group's parts are consecutive.  (Slabs and not
+// parts of each group, since groups are uneven: 8192 rows by 1024 columns in 16
+// groups 21 us, 35 with equal parts of every group.)  Bound by HBM: 10 bytes a
+// value of dy, one pass over each; 2048 x 8192 with GELU 36 us (4.6 TB/s).
 constexpr uint32_t kGradCols = 128;
 
+struct Sums {
+    float s[2][8];
+};
+
 template <int ACT, bool SUM>
-__global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs p, float *out, uint32_t parts) {
-    __shared__ float sh[SUM ? 16 : 1][2][kGradCols + 4];
-    const uint32_t g = blockIdx.y, part = blockIdx.z;
-    uint32_t lo = 0, hi = p.m;
-    if (p.groups) {
-        if (blockIdx.x == 0 && g == 0 && part == 0 && threadIdx.x < 64) check_offsets(p.offsets, p.groups, p.m, p.status);
-        group_range(p.offsets, p.m, g, &lo, &hi);
-    }
-    const uint64_t len = hi - lo;
-    hi = lo + (uint32_t)(len * (part + 1) / parts);
-    lo += (uint32_t)(len * part / parts);
-    const uint32_t x = (threadIdx.x & 15) * 8, y = threadIdx.x >> 4, n = blockIdx.x * kGradCols + x;
-    const uint32_t left = p.n > n ? p.n - n : 0;
-    float s[2][8] = {};
-    if (left) {
-        const auto row = [&](uint32_t i, const float *dy, float *gate, float *rest) {
-            float a[8], b[8];
+__device__ __forceinline__ void grad_row(const GatedGradArgs &p, uint64_t i, uint32_t n, uint32_t left, const float *dy,
+                                         const float *gate, const float *rest, Sums &sums) {
+    float a[8], b[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                a[q] = dy[q] * rest[q] * act_slope<ACT>(gate[q]);
-                b[q] = dy[q] * act_value<ACT>(gate[q]);
-                if constexpr (SUM) {
-                    s[0][q] += a[q];
-                    s[1][q] += b[q];
-                }
-            }
-            store8(p.dz, EC_BF16, i * p.pitch + n, left, a);
-            store8(p.dz, EC_BF16, i * p.pitch + p.n + n, left, b);
-            // the row's zeros, at most seven
-            if (left <= 8)
-                for (uint64_t c = 2 * (uint64_t)p.n; c < p.pitch; ++c) p.dz[i * p.pitch + c] = 0;
-        };
+    for (int q = 0; q < 8; ++q) {
+        a[q] = dy[q] * rest[q] * act_slope<ACT>(gate[q]);
+        b[q] = dy[q] * act_value<ACT>(gate[q]);
+        if constexpr (SUM) {
+            sums.s[0][q] += a[q];
+            sums.s[1][q] += b[q];
+        }
+    }
+    store8(p.dz, EC_BF16, i * p.pitch + n, left, a);
+    store8(p.dz, EC_BF16, i * p.pitch + p.n + n, left, b);
+    if (left <= 8)                          // the row's zeros, at most seven
+        for (uint64_t c = 2 * (uint64_t)p.n; c < p.pitch; ++c) p.dz[i * p.pitch + c] = 0;
+}
+
+// Rows [lo, hi) of one group, their sums to out.
+template <int ACT, bool SUM>
+__device__ __forceinline__ void grad_run(const GatedGradArgs &p, uint32_t column, uint32_t lo, uint32_t hi, float *out) {
+    __shared__ float sh[SUM ? 16 : 1][2][kGradCols + 4];
+    const uint32_t x = (threadIdx.x & 15) * 8, y = threadIdx.x >> 4, n = column + x;
+    const uint32_t left = p.n > n ? p.n - n : 0;
+    Sums sums = {};
+    if (left) {
         uint32_t i = lo + y;
-        for (; i + 16 < hi; i += 32) {      // two rows on the way at a time
+        for (; (uint64_t)i + 16 < hi; i += 32) {        // two rows on the way at a time
             float dy[2][8], gate[2][8], rest[2][8];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -165,38 +183,86 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs p, float 
                 load8_bf16(p.preact, r * p.preact_stride + p.n + n, left, rest[k]);
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) row(i + 16 * k, dy[k], gate[k], rest[k]);
+            for (int k = 0; k < 2; ++k) grad_row<ACT, SUM>(p, i + 16 * k, n, left, dy[k], gate[k], rest[k], sums);
         }
         if (i < hi) {
             float dy[8], gate[8], rest[8];
             load8_bf16(p.dy, (uint64_t)i * p.dy_stride + n, left, dy);
             load8_bf16(p.preact, (uint64_t)i * p.preact_stride + n, left, gate);
             load8_bf16(p.preact, (uint64_t)i * p.preact_stride + p.n + n, left, rest);
-            row(i, dy, gate, rest);
+            grad_row<ACT, SUM>(p, i, n, left, dy, gate, rest, sums);
         }
     }
     if constexpr (SUM) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) sh[y][h][x + q] = s[h][q];
+            for (int q = 0; q < 8; ++q) sh[y][h][x + q] = sums.s[h][q];
         __syncthreads();
-        const uint32_t h = threadIdx.x / kGradCols, c = threadIdx.x % kGradCols, col = blockIdx.x * kGradCols + c;
-        if (col >= p.n) return;
-        float t = 0.0f;
+        const uint32_t h = threadIdx.x / kGradCols, c = threadIdx.x % kGradCols;
+        if (column + c < p.n) {
+            float t = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) t += sh[k][h][c];
-        out[((uint64_t)part * gridDim.y + g) * 2 * p.n + (uint64_t)h * p.n + col] = t;
+            for (int k = 0; k < 16; ++k) t += sh[k][h][c];
+            out[(uint64_t)h * p.n + column + c] = t;
+        }
+        __syncthreads();                    // before the next run's
     }
 }
 
+template <int ACT, bool SUM>
+__global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs p, uint32_t column_blocks) {
+    const uint32_t slab = blockIdx.x / column_blocks, column = (blockIdx.x - slab * column_blocks) * kGradCols;
+    const uint32_t lo = slab * p.slab, hi = (uint32_t)min((uint64_t)lo + p.slab, (uint64_t)p.m);
+    if (!p.groups) {
+        grad_run<ACT, SUM>(p, column, lo, hi, SUM ? p.partial + (uint64_t)slab * 2 * p.n : nullptr);
+        return;
+    }
+    if (blockIdx.x == 0 && threadIdx.x < 64) check_offsets(p.offsets, p.groups, p.m, p.status);
+    // range r holds the rows of group r - 1 (the first and the last those of none)
+    uint32_t edge = 0, start, end, n, sum;
+    for (uint32_t base = 0; base < p.groups + 2 && edge < hi; base += 64) {
+        scan_ranges(p.offsets, p.groups, p.m, p.m, base, edge, 0, &start, &end, &n, &sum);
+        const uint32_t r = base + (threadIdx.x & 63);
+        uint64_t mask = __ballot(r >= 1 && r <= p.groups && start < hi && end > lo && end > start);
+        while (mask) {
+            const int l = __ffsll((unsigned long long)mask) - 1;
+            mask &= mask - 1;
+            const uint32_t a = max(lo, (uint32_t)__builtin_amdgcn_readlane((int)start, l));
+            const uint32_t b = min(hi, (uint32_t)__builtin_amdgcn_readlane((int)end, l)), g = base + l - 1;
+            grad_run<ACT, SUM>(p, column, a, b, SUM ? p.partial + ((uint64_t)slab + g) * 2 * p.n : nullptr);
+        }
+        edge = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+    }
+}
+
+// Adds a group's parts in a fixed order: 16 columns by 16 threads that take
+// every 16th part each.
+__global__ __launch_bounds__(256) void gated_sum_kernel(GatedGradArgs p) {
+    __shared__ float sh[16][17];
+    const uint32_t x = threadIdx.x & 15, y = threadIdx.x >> 4, g = blockIdx.y;
+    const uint64_t c = (uint64_t)blockIdx.x * 16 + x, n = 2 * (uint64_t)p.n;
+    uint32_t lo = 0, hi = p.m;
+    if (p.groups) group_range(p.offsets, p.m, g, &lo, &hi);
+    float s = 0.0f;
+    if (c < n && lo < hi) {
+        const uint64_t last = (hi - 1) / p.slab + (uint64_t)g;
+#pragma unroll 4                            // loads of four parts on the way
+        for (uint64_t q = lo / p.slab + (uint64_t)g + y; q <= last; q += 16) s += p.partial[q * n + c];
+    }
+    sh[y][x] = s;
+    __syncthreads();
+    if (y || c >= n) return;
+    for (int k = 1; k < 16; ++k) s += sh[k][x];
+    p.db[g * n + c] = s;
+}
+
 template <int ACT>
-void launch_grad(const GatedGradArgs &a, uint32_t parts, hipStream_t s) {
-    const dim3 grid((uint32_t)ceil_div(a.n, kGradCols), a.groups ? a.groups : 1, parts);
+void launch_grad(const GatedGradArgs &a, uint32_t column_blocks, uint32_t blocks, hipStream_t s) {
     if (a.db)
-        gated_grad_kernel<ACT, true><<<grid, 256, 0, s>>>(a, parts > 1 ? a.partial : a.db, parts);
+        gated_grad_kernel<ACT, true><<<blocks, 256, 0, s>>>(a, column_blocks);
     else
-        gated_grad_kernel<ACT, false><<<grid, 256, 0, s>>>(a, nullptr, parts);
+        gated_grad_kernel<ACT, false><<<blocks, 256, 0, s>>>(a, column_blocks);
 }
 
 }  // namespace
@@ -212,36 +278,43 @@ hipError_t launch_gated(ProductArgs a, void *workspace, hipStream_t s) {
         case kEven: launch_tiles<Even>(a, q, s); break;
         case kSmall: launch_tiles<Small>(a, q, s); break;
         default:
-            if (a.dtype == EC_E4M3)
-                q.row_tiles == 1 ? launch_few<1, true>(a, q, s) : launch_few<2, true>(a, q, s);
-            else
-                q.row_tiles == 1 ? launch_few<1, false>(a, q, s) : launch_few<2, false>(a, q, s);
+            a.dtype == EC_E4M3 ? launch_few<true>(a, q, s) : launch_few<false>(a, q, s);
     }
     return hipGetLastError();
 }
 
-// Parts of the rows: enough workgroups for the card, each with 32 rows or more (of a group, on average).
-uint32_t gated_grad_parts(const GatedGradArgs &a) {
-    const uint64_t groups = a.groups ? a.groups : 1, blocks = ceil_div(a.n, kGradCols) * groups;
-    uint64_t parts = ceil_div(2048, blocks ? blocks : 1);
-    const uint64_t most = ceil_div(a.m, groups * 32);
-    if (parts > most) parts = most;
-    return (uint32_t)(parts < 1 ? 1 : parts);
+// Rows of a slab: 64, fewer where workgroups would not fill the card, more
+// where parts would be over 1024.
+uint32_t gated_grad_slab(uint32_t m, uint32_t n) {
+    const uint64_t columns = ceil_div(n, kGradCols);
+    uint32_t slab = 64;
+    while (slab > 16 && columns * ceil_div(m, slab) < 1024) slab /= 2;
+    while (ceil_div(m, slab) > 1024) slab *= 2;
+    return slab;
+}
+
+uint64_t gated_grad_workspace(const GatedGradArgs &a) {
+    return a.db ? (ceil_div(a.m, a.slab) + a.groups) * 2 * a.n * 4 : 0;
 }
 
 hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s) {
     if (!a.n) return launch_check_offsets(a.offsets, a.groups, a.m, a.status, s);
-    const uint32_t parts = gated_grad_parts(a);
-    if (!launchable(ceil_div(a.n, kGradCols), 256)) return hipErrorInvalidValue;
-    switch (a.act) {
-        case EC_ACT_GELU: launch_grad<EC_ACT_GELU>(a, parts, s); break;
-        case EC_ACT_SILU: launch_grad<EC_ACT_SILU>(a, parts, s); break;
-        case EC_ACT_RELU: launch_grad<EC_ACT_RELU>(a, parts, s); break;
-        default: launch_grad<EC_ACT_NONE>(a, parts, s);
+    const uint64_t columns = ceil_div(a.n, kGradCols), blocks = columns * ceil_div(a.m, a.slab);
+    const dim3 sums((uint32_t)ceil_div(2 * (uint64_t)a.n, 16), a.groups ? a.groups : 1);
+    if (!launchable(blocks, 256) || !launchable(sums.x, 256)) return hipErrorInvalidValue;
+    if (blocks) {
+        switch (a.act) {
+            case EC_ACT_GELU: launch_grad<EC_ACT_GELU>(a, (uint32_t)columns, (uint32_t)blocks, s); break;
+            case EC_ACT_SILU: launch_grad<EC_ACT_SILU>(a, (uint32_t)columns, (uint32_t)blocks, s); break;
+            case EC_ACT_RELU: launch_grad<EC_ACT_RELU>(a, (uint32_t)columns, (uint32_t)blocks, s); break;
+            default: launch_grad<EC_ACT_NONE>(a, (uint32_t)columns, (uint32_t)blocks, s);
+        }
+    } else {
+        const hipError_t e = launch_check_offsets(a.offsets, a.groups, a.m, a.status, s);
+        if (e != hipSuccess) return e;
     }
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.db || parts == 1) return e;
-    return launch_column_join(a.partial, a.db, (uint64_t)(a.groups ? a.groups : 1) * 2 * a.n, parts, s);
+    if (a.db) gated_sum_kernel<<<sums, 256, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace ec

@@ -371,13 +371,6 @@ hipError_t launch_copy_rows(const void *in, uint64_t stride, uint64_t rows, uint
     return hipGetLastError();
 }
 
-hipError_t launch_column_join(const float *in, float *out, uint64_t n, uint32_t parts, hipStream_t s) {
-    if (!n) return hipSuccess;
-    if (!launchable(ceil_div(n, 256), 256)) return hipErrorInvalidValue;
-    column_join_kernel<<<(uint32_t)ceil_div(n, 256), 256, 0, s>>>(in, out, n, parts);
-    return hipGetLastError();
-}
-
 static uint32_t column_parts(const ColumnSumArgs &a) {
     const uint64_t groups = a.groups ? a.groups : 1, blocks = ceil_div(a.n, kSumCols) * groups;
     uint64_t parts = ceil_div(1024, blocks), most = ceil_div(a.m, groups * 64);
