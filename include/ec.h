@@ -737,7 +737,7 @@ int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream);
  *   dx[m, k] = sum_v G[m, v] w[v, k]        (bf16)
  *   dw[v, k] = sum_m G[m, v] x[m, k]        (dw_dtype)
  * The logits are computed again by pieces of the vocabulary; a piece's G is
- * rounded to bf16 for the products and lies in the workspace (256 MiB, or 8 KiB
+ * rounded to bf16 for the products and lies in the workspace (512 MiB, or 8 KiB
  * a row where that is more), beside x and the fp32 sums of dx.  Fixed order of
  * summation.  k up to 2^24 - 1024.
  */

@@ -79,7 +79,7 @@ struct ProductArgs {
     uint32_t first;                        // kOpLogitGrad: the piece's first column
     const float *sum_in;                   // kOpPieceInput: added to D (as out in type and stride), or null
     // filled in by the plan
-    uint32_t tiles_i, tiles_j, splits;
+    uint32_t tiles_i, tiles_j, splits, blocks;
     float *partial;                        // [splits][tile][TI * TJ] when splits > 1
 };
 

@@ -119,6 +119,16 @@ void launch_few(const ProductArgs &a, const Plan &q, hipStream_t s) {
                      : few_gated_kernel<1, 8, E4M3, false><<<n, 512, 0, s>>>(a);
 }
 
+// A kernel for each activation: all of them in one are more than its registers bear.
+void launch_wide_act(const ProductArgs &a, const Plan &q, hipStream_t s) {
+    switch (a.act) {
+        case EC_ACT_GELU: launch_wide<kOpGated, EC_ACT_GELU>(a, q, s); break;
+        case EC_ACT_SILU: launch_wide<kOpGated, EC_ACT_SILU>(a, q, s); break;
+        case EC_ACT_RELU: launch_wide<kOpGated, EC_ACT_RELU>(a, q, s); break;
+        default: launch_wide<kOpGated, EC_ACT_NONE>(a, q, s);
+    }
+}
+
 template <class T>
 void launch_tiles(const ProductArgs &a, const Plan &q, hipStream_t s) {
     if (a.dtype == EC_E4M3)
@@ -274,9 +284,10 @@ hipError_t launch_gated(ProductArgs a, void *workspace, hipStream_t s) {
     const hipError_t e = place_product(a, q, workspace, s);
     if (e != hipSuccess) return e;
     switch (q.shape) {
-        case kHuge: launch_tiles<Huge>(a, q, s); break;
+        case kHuge: runs_wide(a, q) ? launch_wide_act(a, q, s) : launch_tiles<Huge>(a, q, s); break;
         case kEven: launch_tiles<Even>(a, q, s); break;
         case kSmall: launch_tiles<Small>(a, q, s); break;
+        case kTall: launch_tiles<Tall>(a, q, s); break;
         default:
             a.dtype == EC_E4M3 ? launch_few<true>(a, q, s) : launch_few<false>(a, q, s);
     }

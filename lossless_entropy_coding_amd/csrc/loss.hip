@@ -132,9 +132,10 @@ hipError_t launch_any(ProductArgs a, void *workspace, hipStream_t s) {
     const hipError_t e = place_product(a, q, workspace, s);
     if (e != hipSuccess) return e;
     switch (q.shape) {
-        case kHuge: launch_tiles<Huge, OP>(a, q, s); break;
+        case kHuge: runs_wide(a, q) ? launch_wide<OP, EC_ACT_NONE>(a, q, s) : launch_tiles<Huge, OP>(a, q, s); break;
         case kEven: launch_tiles<Even, OP>(a, q, s); break;
         case kSmall: launch_tiles<Small, OP>(a, q, s); break;
+        case kTall: launch_tiles<Tall, OP>(a, q, s); break;
         default:
             if constexpr (!contracts_b_rows(OP)) {
                 const uint32_t n = (uint32_t)q.blocks;
@@ -170,7 +171,7 @@ ProductArgs forward_product(const LossArgs &p) {
 }
 
 // The pieces of the vocabulary and where the backward pass keeps what.
-constexpr uint64_t kPieceBytes = 256ull << 20;  // of G
+constexpr uint64_t kPieceBytes = 512ull << 20;  // of G
 constexpr uint64_t kLeastPiece = 4096;
 
 struct Pieces {

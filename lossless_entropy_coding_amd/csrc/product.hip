@@ -123,14 +123,17 @@ __global__ __launch_bounds__(64) void check_offsets_kernel(const int32_t *offset
 // What a plan's time is made of, measured on whole runs (us): a stage of one
 // workgroup alone on its CU, a stage per workgroup where every CU is full, and
 // what a workgroup costs besides its stages; bf16 and e4m3.  The full rates
-// are 1.25, 0.87 and 0.51 PFLOP/s in bf16.
+// are 1.25, 0.87, 0.51 and 1.17 PFLOP/s in bf16.  The last, of 129 to 256 rows
+// in a row of as many workgroups as CUs: 160 x 32768 x 2048 maxima and sums 40 us,
+// 46.7 in tiles of 128 x 128; 160 x 2 x 16384 x 2048 gated 36 and 43.
 struct ShapeCost {
     uint32_t TI, TJ, threads, per_cu;
     float alone[2], full[2], fixed;
 };
 constexpr ShapeCost kCost[] = {{256, 256, Huge::THREADS, 1, {0.55f, 1.1f}, {0.86f, 1.5f}, 10.0f},
                                {128, 128, Even::THREADS, 2, {0.25f, 0.43f}, {0.31f, 0.45f}, 5.0f},
-                               {64, 64, Small::THREADS, 3, {0.17f, 0.28f}, {0.133f, 0.18f}, 6.0f}};
+                               {64, 64, Small::THREADS, 3, {0.17f, 0.28f}, {0.133f, 0.18f}, 6.0f},
+                               {256, 128, Tall::THREADS, 1, {0.33f, 0.7f}, {0.46f, 0.85f}, 8.0f}};
 constexpr uint64_t kCUs = 256;
 
 bool aligned(const void *p, uint64_t stride, uint64_t group, uint64_t cols, uint32_t es, bool outer) {
@@ -196,7 +199,7 @@ Plan make_plan(const ProductArgs &a) {
     const uint64_t b_bytes = round_up((outer_a ? 1 : groups) * b_rows * b_pitch * es, 256);
     const uint64_t stages = ceil_div((outer_a ? ceil_div(a.C, groups) : (uint64_t)a.C) * es, kStageBytes);
     float best = 0.0f;
-    for (uint32_t id = kHuge; id <= kSmall; ++id) {
+    for (uint32_t id = kHuge; id <= (a.op >= kOpGated ? kTall : kSmall); ++id) {
         const ShapeCost &c = kCost[id];
         float copies = 0.0f;                            // what this shape has copied and another need not, at 4 TB/s
         bool copy_a = false, copy_b = false;
@@ -257,11 +260,13 @@ void launch_shape(const ProductArgs &a, const Plan &q, hipStream_t s) {
 
 template <class T>
 void launch_op(const ProductArgs &a, const Plan &q, hipStream_t s) {
+    const bool wide = T::TI == Wide::TI && a.act == EC_ACT_NONE && !a.db && runs_wide(a, q);
     if (a.op == EC_LINEAR_GRAD_INPUT)
-        launch_shape<T, EC_LINEAR_GRAD_INPUT, false>(a, q, s);
+        wide ? launch_wide<EC_LINEAR_GRAD_INPUT, EC_ACT_NONE>(a, q, s) : launch_shape<T, EC_LINEAR_GRAD_INPUT, false>(a, q, s);
+    else if (a.op == EC_LINEAR_GRAD_WEIGHT && a.db)
+        launch_shape<T, EC_LINEAR_GRAD_WEIGHT, false, true>(a, q, s);
     else if (a.op == EC_LINEAR_GRAD_WEIGHT)
-        a.db ? launch_shape<T, EC_LINEAR_GRAD_WEIGHT, false, true>(a, q, s)
-             : launch_shape<T, EC_LINEAR_GRAD_WEIGHT, false>(a, q, s);
+        wide ? launch_wide<EC_LINEAR_GRAD_WEIGHT, EC_ACT_NONE>(a, q, s) : launch_shape<T, EC_LINEAR_GRAD_WEIGHT, false>(a, q, s);
     else if (a.dtype == EC_E4M3)
         launch_shape<T, EC_LINEAR_FORWARD, true>(a, q, s);
     else
@@ -315,6 +320,7 @@ hipError_t place_product(ProductArgs &a, const Plan &q, void *workspace, hipStre
     a.tiles_i = q.tiles_i;
     a.tiles_j = q.tiles_j;
     a.splits = q.splits;
+    a.blocks = (uint32_t)q.blocks;
     a.partial = (float *)(ws + q.partial_at);
     return hipSuccess;
 }

@@ -10,6 +10,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) f32x2 lds_f32x2;
 
 // ------------------------------------------------------------- tiled product
 //
@@ -38,6 +39,13 @@ struct Shape {
     static constexpr int NI = TI / WI / 32, NJ = TJ / WJ / 32, W = WI * WJ, THREADS = 64 * W;
     static constexpr int kStage = (TI + TJ) * 64;
 };
+
+using Huge = Shape<256, 256, 2, 4, 4, 1>;
+using Even = Shape<128, 128, 2, 2, 4, 2>;
+using Small = Shape<64, 64, 2, 2, 6, 3>;
+using Tall = Shape<256, 128, 4, 2, 4, 1>;               // of the operators beside ec_linear_op's
+
+enum ShapeId { kHuge, kEven, kSmall, kTall, kFew };
 
 constexpr int kStageBytes = 64;            // of the contraction
 constexpr uint32_t kOutside = 0x80000000u; // an offset past every buffer: reads as zero
@@ -372,7 +380,9 @@ __device__ __forceinline__ void finish_gated(const ProductArgs &p, f32x16 (&acc)
 #pragma unroll
     for (int x = 0; x < NI; ++x) {
         R::put(mem, acc[x], lane);
-#pragma unroll
+        // not unrolled for the large tiles: what follows is long, and the sums must stay in registers
+        constexpr int kUnroll = NI * NJ < 8 ? 32 / kRows : 1;
+#pragma unroll kUnroll
         for (int t = 0; t < 32 / kRows; ++t) {
             const uint32_t row = t * kRows + lane / kLanes, i = i0 + x * 32 + row;
             float gate[8], rest[8], xs = 1.0f;
@@ -399,11 +409,16 @@ __device__ __forceinline__ void finish_gated(const ProductArgs &p, f32x16 (&acc)
 // to bf16 for the matrix units, as every factor of the backward products is.
 __device__ __forceinline__ void finish8_logits(const ProductArgs &p, uint32_t i, uint32_t j, float *v, float2 row,
                                                int32_t target) {
-    const int32_t at = target - (int32_t)(p.first + j);
+    const uint32_t at = (uint32_t)target - (p.first + j);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const float e = __builtin_amdgcn_exp2f((v[q] - row.x) * kLog2E) - (q == at ? 1.0f : 0.0f);
-        v[q] = j + q < p.J ? e * row.y : 0.0f;
+    for (int q = 0; q < 8; ++q) v[q] = __builtin_amdgcn_exp2f((v[q] - row.x) * kLog2E) * row.y;
+    if (at < 8) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] -= q == (int)at ? row.y : 0.0f;
+    }
+    if (j + 8 > p.J) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = j + q < p.J ? v[q] : 0.0f;
     }
     store8(p.out, EC_BF16, i * p.out_stride + j, 8, v);
 }
@@ -426,26 +441,33 @@ __device__ __forceinline__ void finish_logits(const ProductArgs &p, f32x16 (&acc
     }
 }
 
+// With an activation known when compiled.
+template <int NI, int NJ, int OP, int ACT>
+__device__ __forceinline__ void finish_act(const ProductArgs &p, f32x16 (&acc)[NI][NJ], uint32_t g, uint32_t i0,
+                                           uint32_t i1, uint32_t j0, bool zero, lds_char *mem) {
+    if constexpr (OP == kOpLogitGrad)
+        finish_logits<NI, NJ>(p, acc, i0, i1, j0, mem);
+    else if constexpr (OP == kOpGated)
+        finish_gated<NI, NJ, ACT>(p, acc, g, i0, i1, j0, zero, mem);
+    else
+        finish_tiles<NI, NJ, OP, ACT>(p, acc, g, i0, i1, j0, zero, mem);
+}
+
+// Whether an operator's epilogue has an activation.
+template <int OP>
+constexpr bool kActs = OP == EC_LINEAR_FORWARD || OP == EC_LINEAR_GRAD_INPUT || OP == kOpGated;
+
 template <int NI, int NJ, int OP>
 __device__ __forceinline__ void finish(const ProductArgs &p, f32x16 (&acc)[NI][NJ], uint32_t g, uint32_t i0,
                                        uint32_t i1, uint32_t j0, bool zero, lds_char *mem) {
-    if constexpr (contracts_a_rows(OP) || OP == kOpPieceInput) {
-        finish_tiles<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero, mem);
-    } else if constexpr (OP == kOpLogitGrad) {
-        finish_logits<NI, NJ>(p, acc, i0, i1, j0, mem);
-    } else if constexpr (OP == kOpGated) {
-        switch (p.act) {
-            case EC_ACT_GELU: finish_gated<NI, NJ, EC_ACT_GELU>(p, acc, g, i0, i1, j0, zero, mem); break;
-            case EC_ACT_SILU: finish_gated<NI, NJ, EC_ACT_SILU>(p, acc, g, i0, i1, j0, zero, mem); break;
-            case EC_ACT_RELU: finish_gated<NI, NJ, EC_ACT_RELU>(p, acc, g, i0, i1, j0, zero, mem); break;
-            default: finish_gated<NI, NJ, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero, mem);
-        }
+    if constexpr (!kActs<OP>) {
+        finish_act<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero, mem);
     } else {
         switch (p.act) {
-            case EC_ACT_GELU: finish_tiles<NI, NJ, OP, EC_ACT_GELU>(p, acc, g, i0, i1, j0, zero, mem); break;
-            case EC_ACT_SILU: finish_tiles<NI, NJ, OP, EC_ACT_SILU>(p, acc, g, i0, i1, j0, zero, mem); break;
-            case EC_ACT_RELU: finish_tiles<NI, NJ, OP, EC_ACT_RELU>(p, acc, g, i0, i1, j0, zero, mem); break;
-            default: finish_tiles<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero, mem);
+            case EC_ACT_GELU: finish_act<NI, NJ, OP, EC_ACT_GELU>(p, acc, g, i0, i1, j0, zero, mem); break;
+            case EC_ACT_SILU: finish_act<NI, NJ, OP, EC_ACT_SILU>(p, acc, g, i0, i1, j0, zero, mem); break;
+            case EC_ACT_RELU: finish_act<NI, NJ, OP, EC_ACT_RELU>(p, acc, g, i0, i1, j0, zero, mem); break;
+            default: finish_act<NI, NJ, OP, EC_ACT_NONE>(p, acc, g, i0, i1, j0, zero, mem);
         }
     }
 }
@@ -542,15 +564,27 @@ __device__ __forceinline__ Place find_place(const ProductArgs &p, uint32_t block
     return q;
 }
 
+// Tile (x, y) of a wave's sums, laid out by tiles or by pairs of columns of them.
+template <int NI, int NJ>
+__device__ __forceinline__ f32x16 &tile_of(f32x16 (&acc)[NI][NJ], int x, int y) {
+    return acc[x][y];
+}
+
+template <int NI>
+__device__ __forceinline__ f32x16 &tile_of(f32x16 (&acc)[2][NI][2], int x, int y) {
+    return acc[y / 2][x][y % 2];
+}
+
 // Of the tile's columns, each row's maximum and the sum of the exponentials
 // from it, and the logit of the row's target where that is among them.  A
 // wave's accumulators hold row lane % 32 and half of the columns of a 32 x 32
 // tile; the waves side by side are joined in LDS.  A maximum of -inf counts as
 // 0 in the exponent, so that columns of -inf add nothing.
-template <class T>
-__device__ __forceinline__ void finish_stats(const ProductArgs &p, f32x16 (&acc)[T::NI][T::NJ], const Place &q,
-                                             uint32_t wi, uint32_t wave, float2 *mem) {
+template <class T, class ACC>
+__device__ __forceinline__ void finish_stats(const ProductArgs &p, ACC &acc, const Place &q, uint32_t wi, uint32_t wave,
+                                             lds_char *at_mem) {
     constexpr int NI = T::NI, NJ = T::NJ;
+    lds_f32x2 *const mem = (lds_f32x2 *)at_mem;
     const uint32_t lane = threadIdx.x & 63, wj = wave % T::WJ, j0 = q.j0 + wj * (NJ * 32);
     const uint32_t columns = p.J > j0 ? p.J - j0 : 0, half = 4 * (lane >> 5);
 #pragma unroll
@@ -560,33 +594,50 @@ __device__ __forceinline__ void finish_stats(const ProductArgs &p, f32x16 (&acc)
         if (i < q.i1) at = p.target_bytes == 8 ? ((const int64_t *)p.target)[i] : (int64_t)((const int32_t *)p.target)[i];
         at -= (int64_t)j0;
         const uint32_t place = at >= 0 && at < (int64_t)min(columns, NJ * 32u) ? (uint32_t)at : ~0u;
-        float top = -__builtin_inff(), hit = 0.0f;
+        if (columns < NJ * 32) {            // the vocabulary's end
+#pragma unroll
+            for (int y = 0; y < NJ; ++y)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (y * 32 + 8 * (r >> 2) + half + (r & 3) >= columns) tile_of(acc, x, y)[r] = -__builtin_inff();
+        }
+        float hit = 0.0f;
+        if (__ballot(place != ~0u)) {       // seldom, of a large one
+#pragma unroll
+            for (int y = 0; y < NJ; ++y)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    hit = y * 32 + 8 * (r >> 2) + half + (r & 3) == place ? tile_of(acc, x, y)[r] : hit;
+        }
+        // four sums side by side, so that none waits for the one before
+        float tops[4], sums[4] = {};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tops[k] = tile_of(acc, x, 0)[k];
 #pragma unroll
         for (int y = 0; y < NJ; ++y)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const uint32_t c = y * 32 + 8 * (r >> 2) + half + (r & 3);
-                if (c >= columns) acc[x][y][r] = -__builtin_inff();
-                top = fmaxf(top, acc[x][y][r]);
-                hit = c == place ? acc[x][y][r] : hit;
-            }
+            for (int r = 0; r < 16; ++r) tops[r & 3] = fmaxf(tops[r & 3], tile_of(acc, x, y)[r]);
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        top = fmaxf(top, -__builtin_inff());                            // of NaN only
         top = fmaxf(top, __shfl_xor(top, 32));
         const float from = top == -__builtin_inff() ? 0.0f : top;
-        float sum = 0.0f;
 #pragma unroll
         for (int y = 0; y < NJ; ++y)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((acc[x][y][r] - from) * kLog2E);
+            for (int r = 0; r < 16; ++r)
+                sums[r & 3] += __builtin_amdgcn_exp2f((tile_of(acc, x, y)[r] - from) * kLog2E);
+        float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
         sum += __shfl_xor(sum, 32);
         if (place != ~0u && (place & 4) == half) p.hit[i] = hit;
-        if (lane < 32) mem[wj * T::TI + row] = float2{top, sum};
+        if (lane < 32) mem[wj * T::TI + row] = f32x2{top, sum};
     }
     __syncthreads();
-    const uint32_t t = threadIdx.x, i = q.i0 + t;
+    const uint32_t t = threadIdx.x, i = q.i0 + t;       // as many threads as rows, or more
+    static_assert(T::THREADS >= T::TI);
     if (t >= T::TI || i >= q.i1) return;
-    float2 s = mem[t];
+    float2 s = {mem[t][0], mem[t][1]};
 #pragma unroll
-    for (int k = 1; k < T::WJ; ++k) s = join_stats(s, mem[k * T::TI + t]);
+    for (int k = 1; k < T::WJ; ++k) s = join_stats(s, float2{mem[k * T::TI + t][0], mem[k * T::TI + t][1]});
     p.stats[(uint64_t)i * p.tiles_j + q.j0 / T::TJ] = s;
 }
 
@@ -762,10 +813,268 @@ __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
     __syncthreads();                        // every wave has read its last stage
     static_assert(T::W * Turn<NJ>::kBytes <= S * T::kStage, "the turned tiles fit the stages' LDS");
     if constexpr (OP == kOpRowStats)
-        finish_stats<T>(p, acc, q, wi, wave, (float2 *)lds);
+        finish_stats<T>(p, acc, q, wi, wave, (lds_char *)lds);
     else
         finish<NI, NJ, OP>(p, acc, q.group, q.i0 + wi, q.i1, q.j0 + (kGated ? wj / 2 : wj), q.zero,
                            (lds_char *)lds + wave * Turn<NJ>::kBytes);
+}
+
+// ------------------------------------------------------------- wide stages
+//
+// 256 x 256 tiles of bf16 by four waves of 128 x 128, the only ones of their
+// SIMDs: all 512 registers, half of them sums.  A stage is 128 bytes of the
+// contraction, whole lines of either factor; A has two stages in LDS, B, which
+// may come from HBM, three.  The waves read 64 KB of LDS for each 64 KB that is
+// loaded (eight waves of 128 x 64: 96), where LDS gives 128 bytes a clock and the
+// matrix units' full rate would take all of that from eight waves.
+//
+// The matrix instructions are inline assembly, since the compiler moves the sums
+// between registers where it may choose them; a wait follows the last one.  One
+// or two other instructions go between two of them, spread by hand.
+struct Wide {
+    static constexpr int TI = 256, TJ = 256, WI = 2, WJ = 2, NI = 4, NJ = 4, W = 4, THREADS = 64 * W;
+    static constexpr int kSlot = 256 * 128;             // a factor's stage
+    static constexpr int kSlotsA = 2, kSlotsB = 3, kBAt = kSlotsA * kSlot;
+    static constexpr int kDepth = 64, kLoads = 8;       // of the contraction; a wave's loads of a factor's stage
+};
+
+// One factor.  Rows contiguous along the contraction: row r at r * 128, its
+// eight 16-byte chunks in the order chunk ^ (r / 2 % 8).  Contraction
+// outermost: as in Factor.  GATED: 32 rows of the first half of B and 32 of the
+// second by turns, a load's rows in one of them.
+template <bool OUTER, bool GATED>
+struct WideFactor {
+    static constexpr int kHalves = GATED ? 2 : 1;
+    uint32_t off[Wide::kLoads];                         // per lane
+    uint64_t step, base[kHalves];
+    int64_t left[kHalves];
+    i32x4 d[kHalves];
+    uint32_t rest, out;                                 // rest: bytes of a row to come
+
+    // the tile's first row and rows, where the second half begins, and the contraction's range
+    __device__ __forceinline__ void init(const void *p, uint64_t stride, uint64_t row0, uint64_t second, uint32_t rows,
+                                         uint32_t c0, uint32_t c1, uint32_t wave, uint32_t lane) {
+        const uint64_t sb = stride * 2;
+        step = OUTER ? Wide::kDepth * sb : 128;
+        rest = (c1 - c0) * 2;
+#pragma unroll
+        for (int n = 0; n < Wide::kLoads; ++n) {
+            const uint32_t q = n * Wide::W + wave;
+            if constexpr (OUTER) {
+                const uint32_t c = q * 2 + (lane >> 5), pos = lane & 31, h = unit_order(c, 256);
+                off[n] = c * (uint32_t)sb + ((((pos >> 1) ^ h) << 1) | (pos & 1)) * 16;
+            } else {
+                const uint32_t r = q * 8 + (lane >> 3), row = GATED ? r / 64 * 32 + r % 32 : r;
+                off[n] = row * (uint32_t)sb + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+            const uint64_t row = row0 + (h ? second : 0);
+            base[h] = (uint64_t)p + (OUTER ? c0 * sb + row * 2 : row * sb + (uint64_t)c0 * 2);
+            left[h] = OUTER ? ((int64_t)(c1 - c0) - 1) * (int64_t)sb + rows * 2
+                            : ((int64_t)rows - 1) * (int64_t)sb + (int64_t)(c1 - c0) * 2;
+            left[h] = (left[h] + 3) & ~3ll;
+        }
+    }
+
+    // Makes the next stage the one to load, in two parts of a few instructions each and a half.
+    __device__ __forceinline__ void next(int part, uint32_t wave, uint32_t lane) {
+        const int h = part / 2 % kHalves;
+        if (part % 2 == 0) {
+            const int32_t high = (int32_t)(left[h] >> 32);
+            const uint32_t low = (uint32_t)left[h], n = high < 0 ? 0 : high > 0 || low > 0x7FFFFFFFu ? 0x7FFFFFFFu : low;
+            d[h][2] = __builtin_amdgcn_readfirstlane((int)(rest ? n : 0));
+            left[h] -= (int64_t)step;
+        } else {
+            d[h][0] = __builtin_amdgcn_readfirstlane((int)base[h]);
+            d[h][1] = __builtin_amdgcn_readfirstlane((int)(base[h] >> 32) & 0xFFFF);
+            d[h][3] = 0x00027000;
+            base[h] += step;
+            if (h == kHalves - 1) {
+                out = 0;
+                if constexpr (!OUTER) out = ((lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7)) * 16 < rest ? 0 : kOutside;
+                rest = rest > 128 ? rest - 128 : 0;
+            }
+        }
+    }
+
+    // Load k of the stage, to `at` in LDS.  The descriptor was made five
+    // instructions before, or more; m0 needs one wait.
+    __device__ __forceinline__ void load(int k, uint32_t at, uint32_t wave) {
+        const uint32_t q = k * Wide::W + wave;
+        const i32x4 &from = d[GATED ? k & 1 : 0];
+        asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off[k] | out), "s"(from),
+                     "{m0}"(at + q * 1024)
+                     : "memory");
+    }
+
+    __device__ __forceinline__ void load_all(uint32_t at, uint32_t wave, uint32_t lane) {
+#pragma unroll
+        for (int part = 0; part < 2 * kHalves; ++part) next(part, wave, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_nop 4" ::: "memory");
+#pragma unroll
+        for (int k = 0; k < Wide::kLoads; ++k) load(k, at, wave);
+    }
+};
+
+template <bool OUTER>
+struct WideFragments {
+    static __device__ __forceinline__ uint32_t at(uint32_t wave_row, int t, uint32_t lane) {
+        if constexpr (OUTER)
+            return Fragments<256, 4, true>::at(wave_row, t, lane);
+        else
+            return (wave_row + t * 32 + (lane & 31)) * 128 + ((lane >> 5) ^ ((lane >> 1) & 7)) * 16;
+    }
+
+    // Quarter s of tile t.
+    static __device__ __forceinline__ u32x4 read(lds_char *stage, const uint32_t *offs, int t, int s) {
+        if constexpr (OUTER) {
+            union {
+                s16x4 h[2];
+                u32x4 w;
+            } u;
+            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + offs[t] + s * 16 * 512));
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + offs[t] + (s * 16 + 4) * 512));
+            return u.w;
+        } else {
+            return *(lds_u32x4 *)(stage + (offs[0] ^ (s * 32)) + t * 4096);
+        }
+    }
+};
+
+template <int OP, int ACT>
+__global__ __launch_bounds__(Wide::THREADS, 1) void wide_kernel(ProductArgs p) {
+    using T = Wide;
+    constexpr bool kOuterA = contracts_a_rows(OP), kOuterB = contracts_b_rows(OP), kGated = OP == kOpGated;
+    using FA = WideFactor<kOuterA, false>;
+    using FB = WideFactor<kOuterB, kGated>;
+    using RA = WideFragments<kOuterA>;
+    using RB = WideFragments<kOuterB>;
+    __shared__ __attribute__((aligned(1024))) char lds[(T::kSlotsA + T::kSlotsB) * T::kSlot];
+    if (!counts_rows(OP) && p.groups && blockIdx.x == 0 && threadIdx.x < 64)
+        check_offsets(p.offsets, p.groups, kOuterA ? p.C : p.I, p.status);
+    const Place q = find_place<T, OP>(p, blockIdx.x);
+    if (q.none) return;
+    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t wi = wave / 2 * 128, wj = wave % 2 * 128;
+    lds_char *const mem = (lds_char *)lds;
+    // the split's range, in stages of the other tiles, so that its sums are theirs
+    uint32_t c0 = q.c0, c1 = q.c1;
+    if (kJoins<OP> && p.splits > 1) {
+        const uint32_t stages = (c1 + 31) / 32;
+        c0 = (uint32_t)((uint64_t)stages * q.split / p.splits) * 32;
+        c1 = min(c1, (uint32_t)((uint64_t)stages * (q.split + 1) / p.splits) * 32);
+    }
+    f32x16 acc[2][4][2];                                // [64 columns][32 rows][32 columns]
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[h][x][y][r] = 0.0f;
+    if (c1 > c0) {
+        const uint32_t n = (c1 - c0 + T::kDepth - 1) / T::kDepth, mem_at = (uint32_t)(uintptr_t)mem;
+        FA fa;
+        FB fb;
+        fa.init(p.a, kOuterA ? p.a_c : p.a_i, q.i0, 0, q.i1 - q.i0, c0, c1, wave, lane);
+        fb.init((const char *)p.b + (kOuterA ? 0 : q.group * p.b_group * 2), kOuterB ? p.b_c : p.b_j, q.j0, p.J,
+                min(kGated ? 128u : 256u, p.J - q.j0), c0, c1, wave, lane);
+        uint32_t ao[4], bo[4], a_read = 0, b_read = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            ao[t] = RA::at(wi, t, lane);
+            bo[t] = T::kBAt + RB::at(wj, t, lane);
+        }
+        u32x4 af[2][2][4], bf[2][2][4];                 // [half of a stage][quarter of it][tile]
+        const auto read = [&](int r, int half) __attribute__((always_inline)) {     // of 16, in the order of their use
+            const int s = r / 8, t = r % 8;
+            if (t < 4)
+                bf[half][s][t] = RB::read(mem + b_read, bo, t, half * 2 + s);
+            else
+                af[half][s][t - 4] = RA::read(mem + a_read, ao, t - 4, half * 2 + s);
+        };
+        fa.load_all(mem_at, wave, lane);
+        fb.load_all(mem_at + T::kBAt, wave, lane);
+        fb.load_all(mem_at + T::kBAt + T::kSlot, wave, lane);
+        fa.load_all(mem_at + T::kSlot, wave, lane);
+        fb.load_all(mem_at + T::kBAt + 2 * T::kSlot, wave, lane);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * T::kLoads) : "memory");     // the first stage has arrived, everywhere
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int r = 0; r < 16; ++r) read(r, 0);
+        // A stage: in its first half its second half's fragments are read;
+        // then, when every wave has them, its slots take the stages two (A) and
+        // three (B) later, and the next stage's first fragments are read.  At
+        // that point all loads but the last eight, of B two stages ahead, must
+        // have arrived.
+        for (uint32_t k = 0; k < n; ++k) {
+            const uint32_t a_fill = mem_at + a_read, b_fill = mem_at + T::kBAt + b_read;
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int g = 0; g < 64; ++g) {
+                const int half = g / 32, s = g / 16 % 2, x = g / 4 % 4, y = g % 4;
+                if (g == 32) {
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(T::kLoads) : "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    a_read ^= T::kSlot;
+                    b_read = b_read == 2 * T::kSlot ? 0 : b_read + T::kSlot;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
+                             : "+a"(acc[y / 2][x][y % 2])
+                             : "v"(bf[half][s][y]), "v"(af[half][s][x]));
+                if (g % 32 < 16) read(g % 32, 1 - half);
+                if (g == 16 || g == 17) fa.next(g - 16, wave, lane);
+                if (g >= 18 && g < 18 + 2 * FB::kHalves) fb.next(g - 18, wave, lane);
+                if (g >= 32 && g % 2 == 1) {
+                    const int l = (g - 33) / 2;
+                    if (l < T::kLoads)
+                        fa.load(l, a_fill, wave);
+                    else
+                        fb.load(l - T::kLoads, b_fill, wave);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        // nothing is left in flight into this workgroup's LDS; the last products' results
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) asm volatile("" : "+a"(acc[h][x][y]));
+    if (kJoins<OP> && p.splits > 1) {
+        float *o = p.partial + ((uint64_t)q.split * (row_tiles<T, OP>(p) * p.tiles_j) + q.tile) * (T::TI * T::TJ);
+        o += wave * (16 * 1024) + lane * 4;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const f32x16 &v = acc[y / 2][x][y % 2];
+                    *(f32x4 *)(o + ((x * 4 + y) * 4 + r) * 256) = f32x4{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+                }
+        return;
+    }
+    __syncthreads();                                    // every wave has read its last stage
+    if constexpr (OP == kOpRowStats) {
+        finish_stats<T>(p, acc, q, wi, wave, mem);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            finish_act<4, 2, OP, ACT>(p, acc[h], q.group, q.i0 + wi, q.i1, q.j0 + (kGated ? wj / 2 + h * 32 : wj + h * 64), q.zero,
+                                      mem + wave * Turn<2>::kBytes);
+    }
 }
 
 // Adds the splits' sums in their order and finishes: a workgroup takes one
@@ -802,28 +1111,29 @@ __global__ __launch_bounds__(T::THREADS) void join_kernel(ProductArgs p) {
 // columns of the gate and those it is multiplied by.
 template <class T>
 __global__ __launch_bounds__(T::THREADS) void join_gated_kernel(ProductArgs p) {
-    constexpr int NI = T::NI, NJ = T::NJ;
-    __shared__ __attribute__((aligned(1024))) char lds[T::W * Turn<NJ>::kBytes];
-    const uint32_t tile = blockIdx.x / NI, x = blockIdx.x - tile * NI;
+    constexpr int NI = T::NI, N = T::NJ > 2 ? 2 : T::NJ, PAIRS = T::NJ / N;    // 32 x 32 tiles taken at a time
+    __shared__ __attribute__((aligned(1024))) char lds[T::W * Turn<N>::kBytes];
+    const uint32_t part = blockIdx.x % (NI * PAIRS), tile = blockIdx.x / (NI * PAIRS), x = part / PAIRS, pair = part % PAIRS;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t tiles = (uint64_t)p.tiles_i * p.tiles_j;
     uint32_t ti, tj;
     band_order(tile, p.tiles_i, p.tiles_j, &ti, &tj);
-    f32x16 acc[1][NJ] = {};
-    const float *o = p.partial + (uint64_t)tile * (T::TI * T::TJ) + wave * (NI * NJ * 1024) + x * (NJ * 1024) + lane * 4;
+    f32x16 acc[1][N] = {};
+    const float *o = p.partial + (uint64_t)tile * (T::TI * T::TJ) + wave * (NI * T::NJ * 1024) +
+                     (x * T::NJ + pair * N) * 1024 + lane * 4;
 #pragma unroll 2                            // loads of two splits on the way
     for (uint32_t s = 0; s < p.splits; ++s, o += tiles * (T::TI * T::TJ))
 #pragma unroll
-        for (int y = 0; y < NJ; ++y)
+        for (int y = 0; y < N; ++y)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const f32x4 v = *(const f32x4 *)(o + y * 1024 + r * 256);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[0][y][4 * r + k] += v[k];
             }
-    const uint32_t i0 = ti * T::TI, wi = wave / T::WJ * (NI * 32) + x * 32, wj = wave % T::WJ * (NJ * 16);
-    finish<1, NJ, kOpGated>(p, acc, 0, i0 + wi, min(p.I, i0 + T::TI), tj * (T::TJ / 2) + wj, false,
-                            (lds_char *)lds + wave * Turn<NJ>::kBytes);
+    const uint32_t i0 = ti * T::TI, wi = wave / T::WJ * (NI * 32) + x * 32, wj = (wave % T::WJ * T::NJ + pair * N) * 16;
+    finish<1, N, kOpGated>(p, acc, 0, i0 + wi, min(p.I, i0 + T::TI), tj * (T::TJ / 2) + wj, false,
+                           (lds_char *)lds + wave * Turn<N>::kBytes);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -999,14 +1309,6 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(ProductArgs p) {
     }
 }
 
-// ---------------------------------------------------------------------- plan
-
-using Huge = Shape<256, 256, 2, 4, 4, 1>;
-using Even = Shape<128, 128, 2, 2, 4, 2>;
-using Small = Shape<64, 64, 2, 2, 6, 3>;
-
-enum ShapeId { kHuge, kEven, kSmall, kFew };
-
 }  // namespace
 
 // How a product is launched: tiles or few rows, splits of the contraction, copied factors.
@@ -1030,5 +1332,29 @@ Plan make_plan(const ProductArgs &a);
 
 // Copies the factors that the plan has copied and fills in what it decides.
 hipError_t place_product(ProductArgs &a, const Plan &q, void *workspace, hipStream_t s);
+
+namespace {
+
+// Whether the tiles of 256 x 256 are Wide's: where the contraction of a
+// workgroup is long, since four waves take longer for what surrounds it.  50001
+// x 920 x 1000: 147 us so and 124 by eight waves (weight gradient); 32768 x 3690
+// x 2048: 421 and 431.  An epilogue that stores nothing does not weigh: maxima and
+// sums of 1023 x 50001 x 1000 logits 152 and 164 us, 4096 x 131072 x 2048 1902
+// and 2027.
+inline bool runs_wide(const ProductArgs &a, const Plan &q) {
+    return q.shape == kHuge && a.dtype == EC_BF16 && (a.op == kOpRowStats || a.C / (a.groups ? a.groups : q.splits) >= 1536);
+}
+
+template <int OP, int ACT>
+void launch_wide(const ProductArgs &a, const Plan &q, hipStream_t s) {
+    wide_kernel<OP, ACT><<<(uint32_t)q.blocks, Wide::THREADS, 0, s>>>(a);
+    if constexpr (OP == kOpGated) {
+        if (q.splits > 1) join_gated_kernel<Wide><<<q.tiles_i * q.tiles_j * 8, Wide::THREADS, 0, s>>>(a);
+    } else if constexpr (kJoins<OP>) {
+        if (q.splits > 1) join_kernel<Wide, OP><<<q.tiles_i * q.tiles_j * 16, Wide::THREADS, 0, s>>>(a);
+    }
+}
+
+}  // namespace
 
 }  // namespace ec

@@ -299,6 +299,43 @@ def test_stream_and_graph(ec):
         assert all(torch.equal(a, b) for a, b in zip(got, eager)), "replay %d" % k
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("size", [(2048, 1600, 2048), (1500, 1607, 2051), (160, 520, 8200), (250, 1536, 4100)], ids=str)
+def test_large_tiles(ec, size, kind):
+    m, k, n = size
+    g = _gen(13)
+    x, w = _factors(g, m, k, n, kind)
+    s = torch.full((1,), 1e-3, device="cuda") if kind == "e4m3" else None
+    bias = _rand(g, 2 * n, dtype=torch.float32)
+    for act in ("gelu", "silu", "relu", None):
+        y, pre = ec.gated_linear(x, w, bias, act=act, w_scale=s, save_preact=True)
+        want, tol, z, ztol = tr.gated(x, w, bias, act, None, s)
+        near(y, want, tol, "y")
+        near(pre, z, ztol, "preact")
+    if kind == "bf16":
+        dy, pre = _rand(g, m, n), _rand(g, m, 2 * n)
+        got = ec.gated_linear_backward(dy, x, w, pre)
+        for t, (want, tol), name in zip(got, tr.gated_backward(dy, x, w, pre, "silu"), ("dx", "dw", "db")):
+            near(t, want, tol, name)
+
+
+def test_large_tiles_grouped(ec):
+    g = _gen(14)
+    rows, k, n = [1900, 0, 700, 300], 1600, 1030
+    m, off = sum(rows) + 5, edges(rows) + 3
+    x, w = _factors(g, m, k, n, "bf16", len(rows))
+    y = ec.grouped_gated_linear(x, w, off, act="gelu")
+    dy, pre = _rand(g, m, n), _rand(g, m, 2 * n)
+    dx, dw, db = ec.grouped_gated_linear_backward(dy, x, w, off, pre)
+    at = off.tolist()
+    for e in range(len(rows)):
+        s = slice(at[e], at[e + 1])
+        near(y[s], *tr.gated(x[s], w[e], None, "gelu")[:2])
+        for got, (want, tol) in zip((dx[s], dw[e], db[e]), tr.gated_backward(dy[s], x[s], w[e], pre[s], "silu")):
+            near(got, want, tol)
+    assert bool((y[:3] == 0).all()) and bool((y[-2:] == 0).all())
+
+
 def test_contraction_split(ec):
     """Few tiles and a long contraction: sums of parts, joined."""
     g = _gen(11)

@@ -50,7 +50,7 @@ def test_forward_and_backward(ec, size):
 
 
 def test_several_pieces(ec):
-    """A vocabulary of more than one piece (40000 rows: 4096 entries each but the last), with tiles of every row count."""
+    """A vocabulary of more than one piece (40000 rows: 6656 entries, then the rest)."""
     m, k, n = 40000, 16, 9001
     x, w, t, dl = _inputs(m, k, n, 3)
     loss, lse = ec.linear_cross_entropy(x, w, t)
@@ -62,7 +62,7 @@ def test_several_pieces(ec):
     (wx, tx), _ = tr.loss_backward(dl[part], x[part], w, t[part])
     near(dx[part], wx, tx, "dx")
     # every row's share in dw, for some entries of each piece
-    sel = torch.tensor([0, 1, 4095, 4096, 8191, 8192, 9000], device="cuda")
+    sel = torch.tensor([0, 1, 4095, 6655, 6656, 8192, 9000], device="cuda")
     l = tr.mm(x.double(), w[sel].double())
     G = torch.exp(l - lse.double()[:, None])
     G -= (t[:, None] == sel[None, :]).double()
@@ -71,6 +71,19 @@ def test_several_pieces(ec):
     ww = tr.mm(G.t().contiguous(), x.double().t().contiguous())
     # G off by 2^-8 of itself, and by what lse's rounding (2^-24 of about 9) and the logits' make of it
     near(dw[sel], ww, mag * (2.0 ** -8 + 64 * tr.U) + tr.sum_error(m, mag) + tr.U * ww.abs(), "dw")
+
+
+@pytest.mark.parametrize("size", [(2100, 1600, 4200), (1900, 1607, 3001), (160, 520, 16500), (256, 1536, 9000)], ids=str)
+def test_large_tiles(ec, size):
+    x, w, t, dl = _inputs(*size, seed=13)
+    loss, lse = ec.linear_cross_entropy(x, w, t)
+    want, tol, want_lse, tol_lse, _, _ = tr.loss(x, w, t)
+    near(lse, want_lse, tol_lse, "lse")
+    near(loss, want, tol, "loss")
+    dx, dw = ec.linear_cross_entropy_backward(dl, x, w, t, lse)
+    (wx, tx), (ww, tw) = tr.loss_backward(dl, x, w, t)
+    near(dx, wx, tx, "dx")
+    near(dw, ww, tw, "dw")
 
 
 def test_targets(ec):
