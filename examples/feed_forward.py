@@ -11,6 +11,11 @@ needs, then the gradients of the input and of every parameter.  `serve_experts`
 routes each row to one of several experts and runs their first products as one
 grouped product.
 
+`GatedModel` is a gated layer under a vocabulary, trained step by step:
+
+    a    = GELU(h Wg^T) * (h Wu^T),   y = a W2^T + x,   loss over y V^T
+    AdamW over the fp32 masters, its states as e4m3 bytes; the layer works with their bf16 copies
+
     python examples/feed_forward.py [rows] [width] [hidden]
 """
 
@@ -94,6 +99,50 @@ def serve_experts(x, router, w1, b1):
     return torch.empty_like(y).index_copy_(0, order, y), choice
 
 
+class GatedModel:
+    """fp32 masters, the bf16 weights that the layer works with, and the optimizer's state."""
+
+    def __init__(self, width, hidden, vocabulary, device="cuda", seed=0):
+        g = torch.Generator(device=device).manual_seed(seed)
+
+        def normal(*shape, scale):
+            return torch.randn(shape, generator=g, device=device) * scale
+
+        self.masters = [normal(2 * hidden, width, scale=width ** -0.5), normal(width, hidden, scale=hidden ** -0.5),
+                        normal(vocabulary, width, scale=width ** -0.5), 1 + normal(width, scale=0.1), normal(width, scale=0.1)]
+        self.weights = [p.bfloat16() for p in self.masters[:3]]
+        self.state = ec.adamw_state(self.masters, torch.uint8)
+
+    def gradients(self, x, target):
+        """(mean loss, gradients of the masters) of x's rows [rows, width] (bf16); targets of -100 are left out."""
+        w1, w2, vocabulary = self.weights
+        gain, shift = self.masters[3:]
+        h, mean, rstd = ec.layer_norm(x, gain, shift)
+        a, z = ec.gated_linear(h, w1, act="gelu", save_preact=True)
+        y = ec.linear(a, w2, residual=x)
+        loss, lse = ec.linear_cross_entropy(y, vocabulary, target)
+        each = 1 / (target != -100).sum(dtype=torch.float32).clamp(min=1).reshape(1)
+        dy, dvocabulary = ec.linear_cross_entropy_backward(each, y, vocabulary, target, lse)
+        da, dw2, _ = ec.linear_backward(dy, a, w2, need_db=False)
+        dh, dw1, _ = ec.gated_linear_backward(da, h, w1, z, act="gelu", need_db=False)
+        _, dgain, dshift = ec.layer_norm_backward(dh, x, mean, rstd, gain, residual_grad=dy)
+        return loss.sum() * each, [dw1, dw2, dvocabulary, dgain, dshift]
+
+    def step(self, x, target, lr=1e-3):
+        loss, grads = self.gradients(x, target)
+        ec.adamw(self.masters, grads, self.state, lr=lr, weight_decay=[0.1, 0.1, 0.1, 0, 0], copies=self.weights + [None, None])
+        return loss
+
+    def coded_state(self):
+        """Bytes of the optimizer's e4m3 states, and of the streams they are coded to."""
+        plain = coded = 0
+        for s in (self.state.m, self.state.v):
+            cb = ec.Codebook.huffman(ec.byte_histogram(s)[0].cpu().tolist())
+            plain += s.numel()
+            coded += int(ec.encode(cb, s, CHUNK)[1].item())
+        return plain, coded
+
+
 def main(rows=512, width=2048, hidden=8192):
     layer = Layer(width, hidden)
     x = torch.randn(rows, width, device="cuda").bfloat16()
@@ -108,6 +157,10 @@ def main(rows=512, width=2048, hidden=8192):
     router = (torch.randn(experts, width, device="cuda") * width ** -0.5).bfloat16()
     y, choice = serve_experts(x, router, w1, None)
     print("experts: rows %s" % torch.bincount(choice, minlength=experts).tolist())
+    model = GatedModel(width, hidden // 2, 4 * hidden)
+    target = torch.randint(4 * hidden, (rows,), device="cuda")
+    losses = [float(model.step(x, target)) for _ in range(4)]
+    print("gated: losses %s; optimizer states %d bytes, coded %d" % ((["%.3f" % v for v in losses],) + model.coded_state()))
 
 
 if __name__ == "__main__":

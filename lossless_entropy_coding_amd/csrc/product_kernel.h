@@ -25,8 +25,8 @@ typedef __attribute__((address_space(3))) f32x2 lds_f32x2;
 // the matrix units' time at their full rate, 128 x 128: all of it), and the
 // power limit, which brings the clock under full load from 2.4 to 1.6 - 2.0
 // GHz (the same product of zeros runs 1.25 times as fast).  Eight waves of
-// 128 x 64 keep two waves a SIMD; four of 128 x 128 need all registers and
-// spill.  4096 x 16384 x 2048 bf16 with GELU and e4m3 output: 306 us (0.90
+// 128 x 64 keep two waves a SIMD (four of 128 x 128 need all registers: Wide).
+// 4096 x 16384 x 2048 bf16 with GELU and e4m3 output: 306 us (0.90
 // PFLOP/s; 300 to 315 by card); 4096 x 2048 x 16384 e4m3: 224 us with the join
 // (1.2); backward of 2048 x 16384 x 2048: 288 us (0.95).  One workgroup a CU
 // leaves its first loads and its epilogue exposed: 30% of the waves' time is
@@ -824,9 +824,15 @@ __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
 // 256 x 256 tiles of bf16 by four waves of 128 x 128, the only ones of their
 // SIMDs: all 512 registers, half of them sums.  A stage is 128 bytes of the
 // contraction, whole lines of either factor; A has two stages in LDS, B, which
-// may come from HBM, three.  The waves read 64 KB of LDS for each 64 KB that is
-// loaded (eight waves of 128 x 64: 96), where LDS gives 128 bytes a clock and the
-// matrix units' full rate would take all of that from eight waves.
+// may come from HBM, three.  The waves read 128 KB of LDS for the 64 KB of a stage
+// (eight waves of 128 x 64: 192); LDS gives 128 bytes a clock, and with what is
+// written the matrix units' full rate would take all of that from eight waves.
+// Logits of 4096 x 32768 x 8192, maxima and sums only: 1.36 PFLOP/s (1.99 of
+// zeros, without the power limit), by eight waves 1.23 (1.59).  What is left is
+// the first loads and the epilogue, some 10 us a tile (4096 x 32768 x 2048: 1.17,
+// of zeros 1.65).  One workgroup a CU that goes from tile to tile, the next one's
+// first stages on the way during the epilogue, was slower by 5 to 10%: what it
+// has to decide stands between the matrix instructions of the one wave of a SIMD.
 //
 // The matrix instructions are inline assembly, since the compiler moves the sums
 // between registers where it may choose them; a wait follows the last one.  One
@@ -1342,7 +1348,8 @@ namespace {
 // sums of 1023 x 50001 x 1000 logits 152 and 164 us, 4096 x 131072 x 2048 1902
 // and 2027.
 inline bool runs_wide(const ProductArgs &a, const Plan &q) {
-    return q.shape == kHuge && a.dtype == EC_BF16 && (a.op == kOpRowStats || a.C / (a.groups ? a.groups : q.splits) >= 1536);
+    const uint32_t parts = contracts_a_rows(a.op) && a.groups ? a.groups : q.splits;
+    return q.shape == kHuge && a.dtype == EC_BF16 && (a.op == kOpRowStats || a.C / parts >= 1536);
 }
 
 template <int OP, int ACT>

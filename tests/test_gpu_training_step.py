@@ -2,10 +2,14 @@
 the residual, loss, backward pass and weight update, in bf16 with fp32 masters,
 against the same step in 64 bits, and captured into a graph."""
 
+import importlib.util
+import os
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
+import _ffn  # noqa: E402
 import _training as tr  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -150,3 +154,42 @@ def test_states_travel_coded(ec):
         back, status2 = ec.decode(cb, out[: int(out_len.item())], s.numel())
         torch.cuda.synchronize()
         assert int(status) == int(status2) == 0 and torch.equal(back, s) and int(out_len) < s.numel()
+
+
+@pytest.mark.parametrize("m,n,k", [(2048, 1600, 4096), (4100, 1537, 2049), (1600, 8200, 2048), (6000, 2048, 264)])
+def test_long_contractions(ec, m, n, k):
+    """The backward products of long contractions, which run in tiles of their own, split and not."""
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    dy, w, x = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((m, n), (n, k), (m, k)))
+    dx, dw, _ = ec.linear_backward(dy, x, w, need_db=False, dw_dtype=torch.float32)
+    _ffn.near(dx, *_ffn.grad_input(dy, w), "dx")
+    _ffn.near(dw, *_ffn.grad_weight(dy, x, torch.float32), "dw")
+    again = ec.linear_backward(dy, x, w, need_db=False, dw_dtype=torch.float32)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+def test_example(ec):
+    """examples/feed_forward.py's gated model runs, and its gradients are those of the formulas."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("feed_forward", os.path.join(root, "examples", "feed_forward.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model = example.GatedModel(WIDTH, HIDDEN, VOCABULARY)
+    x, t = _data()
+    loss, grads = model.gradients(x, t)
+    leaves = [v.double().requires_grad_() for v in model.weights + model.masters[3:]]
+    w1, w2, vocabulary, gain, shift = leaves
+    h = torch.nn.functional.layer_norm(x.double(), (WIDTH,), gain, shift)
+    z = h @ w1.t()
+    y = (tr.act(z[:, :HIDDEN], "gelu") * z[:, HIDDEN:]) @ w2.t() + x.double()
+    want = torch.nn.functional.cross_entropy(y @ vocabulary.t(), t)
+    want.backward()
+    assert abs(float(loss) / float(want.detach()) - 1) < 8 * 2.0 ** -8
+    for a, b in zip(grads, leaves):
+        assert _off(a, b.grad) < 8 * 2.0 ** -8          # as in test_gradients
+    before = [p.clone() for p in model.masters]
+    model.step(x, t)
+    assert not any(torch.equal(p, q) for p, q in zip(before, model.masters))
+    assert all(torch.equal(w, p.bfloat16()) for w, p in zip(model.weights, model.masters))
+    plain, coded = model.coded_state()
+    assert plain == 2 * model.state.m.numel() and 0 < coded
