@@ -688,7 +688,8 @@ int gated_linear_forward(const ec_linear_args *a, hipStream_t stream);
  *   dw[2n, k] = sum_m dz[m, j] x[m, k]      (out_dtype EC_BF16 or EC_FP32, when d_dw; reads d_x)
  *   db[2n]    = sum_m dz[m, j]              (fp32, when d_db; of dz before its rounding)
  * dz is rounded to bf16 for the two products and lies in the workspace.  n up
- * to 2^23 - 512, k up to 2^25 - 2048.  Outputs overlap nothing that is read.
+ * to 2^23 - 512, k up to 2^25 - 2048 (EC_E_UNSUPPORTED beyond).  Outputs overlap
+ * nothing that is read.
  */
 uint64_t gated_linear_grad_workspace_bytes(const ec_linear_args *a);
 int gated_linear_grad(const ec_linear_args *a, hipStream_t stream);
@@ -727,7 +728,7 @@ typedef struct ec_loss_args {
 /*
  * lse[m]  = log sum_v exp(l[m, v])
  * loss[m] = lse[m] - l[m, target[m]]
- * Products and sums in fp32.
+ * Products and sums in fp32.  m up to 2^24 - 1 (EC_E_UNSUPPORTED beyond).
  */
 uint64_t linear_cross_entropy_workspace_bytes(const ec_loss_args *a);
 int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream);
@@ -739,7 +740,8 @@ int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream);
  * The logits are computed again by pieces of the vocabulary; a piece's G is
  * rounded to bf16 for the products and lies in the workspace (512 MiB, or 8 KiB
  * a row where that is more), beside x and the fp32 sums of dx.  Fixed order of
- * summation.  k up to 2^24 - 1024.
+ * summation.  k up to 2^24 - 1024, m k below 2^35 (EC_E_UNSUPPORTED beyond).
+ * Outputs overlap nothing that is read.
  */
 uint64_t linear_cross_entropy_grad_workspace_bytes(const ec_loss_args *a);
 int linear_cross_entropy_grad(const ec_loss_args *a, hipStream_t stream);
@@ -749,7 +751,7 @@ int linear_cross_entropy_grad(const ec_loss_args *a, hipStream_t stream);
  *   g = grad * *d_grad_scale,  t = *d_steps + 1
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32; then copy = bf16(p) where given, and *d_steps = t.
+ * in fp32; then copy = bf16(p) where given, and *d_steps = t (below 2^31 - 1).
  *
  * The states of all tensors lie in d_m and d_v, in blocks of EC_ADAMW_BLOCK
  * values: tensor i's begin at the sum of adamw_state_blocks(n) of those before

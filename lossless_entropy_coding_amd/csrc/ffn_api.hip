@@ -435,7 +435,7 @@ GatedGrad gated_grad(const ec_linear_args *a, void *workspace) {
 }
 
 bool runs(const GatedGrad &q, const ec_linear_args *a) {
-    return (!a->d_dx || product_fits(q.dx)) && (!a->d_dw || product_fits(q.dw));
+    return gated_grad_fits(q.grad) && (!a->d_dx || product_fits(q.dx)) && (!a->d_dw || product_fits(q.dw));
 }
 
 }  // namespace

@@ -119,6 +119,7 @@ struct GatedGradArgs {
 
 hipError_t launch_gated(ProductArgs a, void *workspace, hipStream_t s);
 uint32_t gated_grad_slab(uint32_t m, uint32_t n);
+bool gated_grad_fits(const GatedGradArgs &a);
 uint64_t gated_grad_workspace(const GatedGradArgs &a);
 hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s);
 

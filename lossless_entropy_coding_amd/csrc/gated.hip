@@ -295,13 +295,18 @@ hipError_t launch_gated(ProductArgs a, void *workspace, hipStream_t s) {
 }
 
 // Rows of a slab: 64, fewer where workgroups would not fill the card, more
-// where parts would be over 1024.
+// where parts would be over 1024 or workgroups too many for a launch.
 uint32_t gated_grad_slab(uint32_t m, uint32_t n) {
     const uint64_t columns = ceil_div(n, kGradCols);
     uint32_t slab = 64;
     while (slab > 16 && columns * ceil_div(m, slab) < 1024) slab /= 2;
-    while (ceil_div(m, slab) > 1024) slab *= 2;
+    while (ceil_div(m, slab) > 1024 || (slab < m && !launchable(columns * ceil_div(m, slab), 256))) slab *= 2;
     return slab;
+}
+
+bool gated_grad_fits(const GatedGradArgs &a) {
+    return launchable(ceil_div(a.n, kGradCols) * ceil_div(a.m, a.slab), 256) &&
+           (!a.db || launchable(ceil_div(2 * (uint64_t)a.n, 16), 256));
 }
 
 uint64_t gated_grad_workspace(const GatedGradArgs &a) {
@@ -312,7 +317,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s) {
     if (!a.n) return launch_check_offsets(a.offsets, a.groups, a.m, a.status, s);
     const uint64_t columns = ceil_div(a.n, kGradCols), blocks = columns * ceil_div(a.m, a.slab);
     const dim3 sums((uint32_t)ceil_div(2 * (uint64_t)a.n, 16), a.groups ? a.groups : 1);
-    if (!launchable(blocks, 256) || !launchable(sums.x, 256)) return hipErrorInvalidValue;
+    if (!gated_grad_fits(a)) return hipErrorInvalidValue;
     if (blocks) {
         switch (a.act) {
             case EC_ACT_GELU: launch_grad<EC_ACT_GELU>(a, (uint32_t)columns, (uint32_t)blocks, s); break;

@@ -1346,9 +1346,12 @@ namespace {
 // x 920 x 1000: 147 us so and 124 by eight waves (weight gradient); 32768 x 3690
 // x 2048: 421 and 431.  An epilogue that stores nothing does not weigh: maxima and
 // sums of 1023 x 50001 x 1000 logits 152 and 164 us, 4096 x 131072 x 2048 1902
-// and 2027.
+// and 2027.  Where the contraction is outermost a stage's 64 rows must be within
+// 2 GiB, twice what the other tiles' 32 need.
 inline bool runs_wide(const ProductArgs &a, const Plan &q) {
     const uint32_t parts = contracts_a_rows(a.op) && a.groups ? a.groups : q.splits;
+    const auto far = [](uint64_t stride) { return Wide::kDepth * stride * 2 + 65536 >= 1ull << 31; };
+    if ((contracts_a_rows(a.op) && far(a.a_c)) || (contracts_b_rows(a.op) && far(a.b_c))) return false;
     return q.shape == kHuge && a.dtype == EC_BF16 && (a.op == kOpRowStats || a.C / parts >= 1536);
 }
 

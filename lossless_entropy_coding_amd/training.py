@@ -18,8 +18,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .ffn import (_BF16, _DTYPES, _E4M3, _FP32, _current_device, _ec, _empty, _error, _given, _matrix, _placed, _row_stride, _run, _status,
-                  _vector, _warn_unrecorded)
+from .ffn import (_BF16, _DTYPES, _E4M3, _FP32, _current_device, _ec, _empty, _error, _given, _matrix, _placed, _row_stride,
+                  _run, _status, _vector, _warn_unrecorded)
 
 _vp, _u64, _u32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32
 
@@ -183,6 +183,8 @@ def adamw_state(params, state_dtype=torch.float32) -> AdamWState:
     if state_dtype not in (torch.float32, torch.float8_e4m3fn, torch.uint8):
         _error("state_dtype must be float32, float8_e4m3fn or uint8 (e4m3 bytes), not %s" % state_dtype)
     blocks, dev = sum(_blocks(p.numel()) for p in params), params[0].device
+    if any(p.device != dev for p in params):
+        _error("params must be on one device")
     n, coded = blocks * ADAMW_BLOCK, state_dtype != torch.float32
 
     def zeros():
@@ -277,6 +279,8 @@ def adamw(params, grads, state: AdamWState, *, lr=1e-3, betas=(0.9, 0.999), eps=
             copy = c.data_ptr()
         words += (p.data_ptr(), g.data_ptr(), copy, n, decay)
         blocks += (n + 255) >> 8
+    if not isinstance(state, (list, tuple)) or len(state) != 5:
+        _error("state must be an AdamWState")
     m, v, m_scale, v_scale, steps = state
     length = ((blocks * ADAMW_BLOCK,),)
     _vector(m, "state.m", length, _STATES, dev)
@@ -299,9 +303,11 @@ def adamw(params, grads, state: AdamWState, *, lr=1e-3, betas=(0.9, 0.999), eps=
         grad_scale = grad_scale.data_ptr()
     if not isinstance(seed, int) or not 0 <= seed < 1 << 32:
         _error("seed must be a whole number of 32 bits, not %r" % (seed,))
+    if not isinstance(betas, (list, tuple)) or len(betas) != 2:
+        _error("betas must be two numbers")
     beta1, beta2 = betas
-    a = _AdamWArgs(m.data_ptr(), v.data_ptr(), *scales, blocks, steps.data_ptr(), lr_at, grad_scale, _number(lr, "lr", 0.0),
-                   _number(beta1, "betas[0]", 0.0, 1.0), _number(beta2, "betas[1]", 0.0, 1.0), _number(eps, "eps", 0.0), kind,
+    a = _AdamWArgs(m.data_ptr(), v.data_ptr(), *scales, blocks, steps.data_ptr(), lr_at, grad_scale, _number(lr, "lr", 0.0, 1e38),
+                   _number(beta1, "betas[0]", 0.0, 1.0), _number(beta2, "betas[1]", 0.0, 1.0), _number(eps, "eps", 0.0, 1e38), kind,
                    seed)
     ec = _ec()
     tensors = array.array("Q", words)

@@ -168,6 +168,18 @@ def test_long_contractions(ec, m, n, k):
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
+def test_far_rows(ec):
+    """Rows of the contraction 32.4 MiB apart: 32 of them are within 2 GiB, 64 are not."""
+    m, n, k, stride = 8192, 1600, 2048, 17_000_000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = torch.empty((n - 1) * stride + k, dtype=torch.bfloat16, device="cuda").as_strided((n, k), (stride, 1))
+    w.copy_(torch.randn((n, k), generator=g, device="cuda"))
+    dy = torch.randn((m, n), generator=g, device="cuda").bfloat16()
+    dx = ec.linear_backward(dy, None, w, need_dw=False, need_db=False)[0]
+    assert torch.equal(dx, ec.linear_backward(dy, None, w.contiguous(), need_dw=False, need_db=False)[0])
+    _ffn.near(dx[::97], *_ffn.grad_input(dy[::97], w), "dx")
+
+
 def test_example(ec):
     """examples/feed_forward.py's gated model runs, and its gradients are those of the formulas."""
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))

@@ -68,6 +68,9 @@ def test_gated_grad_workspace(ec):
     # rows that no tile of the input's gradient reaches
     a = _gated(preact=0x70000, preact_stride=1 << 25, n=1 << 24, dy_stride=1 << 24)
     assert ec.lib().gated_linear_grad(ctypes.byref(a), None) == UNSUPPORTED
+    # sums of more columns than a launch has threads for
+    a = _gated(preact=0x70000, preact_stride=1 << 29, n=1 << 28, dy_stride=1 << 28, dx=0, dw=0, db=0x1000)
+    assert ec.lib().gated_linear_grad(ctypes.byref(a), None) == UNSUPPORTED
 
 
 def _loss(**kw):
@@ -110,6 +113,9 @@ def test_loss_workspaces(ec):
     need = ec.lib().linear_cross_entropy_workspace_bytes(ctypes.byref(_loss()))
     a = _loss(workspace=0x1000000, workspace_bytes=need - 1)
     assert ec.lib().linear_cross_entropy(ctypes.byref(a), None) == INVAL
+    assert ec.lib().linear_cross_entropy(ctypes.byref(_loss(m=1 << 24, workspace=0x1000000)), None) == UNSUPPORTED
+    wide = dict(m=1 << 23, k=1 << 13, x_stride=1 << 13, w_stride=1 << 13, dx_stride=1 << 13, dw_stride=1 << 13)
+    assert ec.lib().linear_cross_entropy_grad(ctypes.byref(_loss(**wide)), None) == UNSUPPORTED
     long = dict(k=1 << 28, x_stride=1 << 28, w_stride=1 << 28, dx_stride=1 << 28, dw_stride=1 << 28)
     assert ec.lib().linear_cross_entropy_grad(ctypes.byref(_loss(**long)), None) == UNSUPPORTED
     # the room for a piece of the gradient does not grow with the vocabulary
@@ -207,7 +213,8 @@ def test_binding_refuses(ec):
         lambda: ec.adamw([f], [f], state, seed=1 << 32), lambda: ec.adamw([f], [f], state, grad_scale=f),
         lambda: ec.adamw([f], [f], coded._replace(m_scale=None)), lambda: ec.adamw([f], [f], state._replace(v=coded.v)),
         lambda: ec.adamw([f], [f], state._replace(steps=s)), lambda: ec.adamw([f], [f], state._replace(m=state.m[:100])),
-        lambda: ec.adamw([f[::2]], [f[:2]], state), lambda: ec.adamw([f], None, state),
+        lambda: ec.adamw([f[::2]], [f[:2]], state), lambda: ec.adamw([f], None, state), lambda: ec.adamw([f], [f], None),
+        lambda: ec.adamw([f], [f], state[:3]), lambda: ec.adamw([f], [f], state, betas=0.9), lambda: ec.adamw([f], [f], state, lr=1e39),
     ]
     for k, call in enumerate(refused):
         with pytest.raises(ec.ECError):
