@@ -141,6 +141,26 @@ def test_captured_step(ec, state):
         assert all(torch.equal(a, b) for a, b in zip(one.masters + one.weights, two.masters + two.weights)), "replay %d" % k
 
 
+def test_two_at_once(ec):
+    """Two models step on two streams at the same time: as one after the other."""
+    models = [Model(ec, torch.uint8, seed) for seed in (1, 2)]
+    alone = [Model(ec, torch.uint8, seed) for seed in (1, 2)]
+    data = [_data(3), _data(4)]
+    streams = [torch.cuda.Stream() for _ in models]
+    torch.cuda.synchronize()
+    for k in range(4):
+        for model, (x, t), s in zip(models, data, streams):
+            with torch.cuda.stream(s):
+                model.step(ec, x, t)
+    torch.cuda.synchronize()
+    for model, (x, t) in zip(alone, data):
+        for k in range(4):
+            model.step(ec, x, t)
+    for a, b in zip(models, alone):
+        assert all(torch.equal(p, q) for p, q in zip(a.masters + a.weights, b.masters + b.weights))
+        assert torch.equal(a.state.m, b.state.m) and torch.equal(a.state.v, b.state.v)
+
+
 def test_states_travel_coded(ec):
     """An optimizer's e4m3 states are tensor bytes like any other: coded and decoded they are the same."""
     model = Model(ec, torch.uint8)
