@@ -740,7 +740,7 @@ int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream);
  * The logits are computed again by pieces of the vocabulary; a piece's G is
  * rounded to bf16 for the products and lies in the workspace (512 MiB, or 8 KiB
  * a row where that is more), beside x and the fp32 sums of dx.  Fixed order of
- * summation.  k up to 2^24 - 1024, m k below 2^35 (EC_E_UNSUPPORTED beyond).
+ * summation.  m up to 2^26 - 4, k up to 2^24 - 1024 (EC_E_UNSUPPORTED beyond).
  * Outputs overlap nothing that is read.
  */
 uint64_t linear_cross_entropy_grad_workspace_bytes(const ec_loss_args *a);

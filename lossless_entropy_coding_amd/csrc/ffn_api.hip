@@ -384,6 +384,7 @@ struct GatedGrad {
     GatedGradArgs grad;
     ProductArgs dx, dw;
     uint64_t partial, product, bytes;       // workspace
+    bool fits;
 };
 
 GatedGrad gated_grad(const ec_linear_args *a, void *workspace) {
@@ -409,6 +410,8 @@ GatedGrad gated_grad(const ec_linear_args *a, void *workspace) {
     q.product = q.partial + (gated_grad_workspace(g) + 255) / 256 * 256;
     g.partial = (float *)(ws + q.partial);
     q.bytes = q.product;
+    q.fits = gated_grad_fits(g);
+    uint64_t need;
     // the products of dz, as of the gradient of a product with 2 n columns
     ec_linear_args l = *a;
     l.n = 2 * a->n;
@@ -422,20 +425,16 @@ GatedGrad gated_grad(const ec_linear_args *a, void *workspace) {
         q.dx = product(&l, EC_LINEAR_GRAD_INPUT);
         q.dx.a_i = g.pitch;
         q.dx.a_padded = true;
-        const uint64_t need = q.product + product_workspace(q.dx);
-        q.bytes = need > q.bytes ? need : q.bytes;
+        q.fits = product_need(q.dx, &need) && q.fits;
+        q.bytes = q.product + need > q.bytes ? q.product + need : q.bytes;
     }
     if (a->d_dw) {
         q.dw = product(&l, EC_LINEAR_GRAD_WEIGHT);
         q.dw.a_c = g.pitch;
-        const uint64_t need = q.product + product_workspace(q.dw);
-        q.bytes = need > q.bytes ? need : q.bytes;
+        q.fits = product_need(q.dw, &need) && q.fits;
+        q.bytes = q.product + need > q.bytes ? q.product + need : q.bytes;
     }
     return q;
-}
-
-bool runs(const GatedGrad &q, const ec_linear_args *a) {
-    return gated_grad_fits(q.grad) && (!a->d_dx || product_fits(q.dx)) && (!a->d_dw || product_fits(q.dw));
 }
 
 }  // namespace
@@ -449,8 +448,8 @@ int gated_linear_forward(const ec_linear_args *a, hipStream_t stream) {
     const int rc = check_gated(a);
     if (rc) return rc;
     const ProductArgs p = gated_product(a);
-    if (!product_fits(p)) return EC_E_UNSUPPORTED;
-    const uint64_t need = product_workspace(p);
+    uint64_t need;
+    if (!product_need(p, &need)) return EC_E_UNSUPPORTED;
     if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;
     return hip_code(launch_gated(p, a->d_workspace, stream));
 }
@@ -458,14 +457,14 @@ int gated_linear_forward(const ec_linear_args *a, hipStream_t stream) {
 uint64_t gated_linear_grad_workspace_bytes(const ec_linear_args *a) {
     if (check_gated_grad(a)) return 0;
     const GatedGrad q = gated_grad(a, nullptr);
-    return runs(q, a) ? q.bytes : 0;
+    return q.fits ? q.bytes : 0;
 }
 
 int gated_linear_grad(const ec_linear_args *a, hipStream_t stream) {
     const int rc = check_gated_grad(a);
     if (rc) return rc;
     const GatedGrad q = gated_grad(a, a->d_workspace);
-    if (!runs(q, a)) return EC_E_UNSUPPORTED;
+    if (!q.fits) return EC_E_UNSUPPORTED;
     if (q.bytes && (!a->d_workspace || a->workspace_bytes < q.bytes)) return EC_E_INVAL;
     hipError_t e = launch_gated_grad(q.grad, stream);
     char *const ws = (char *)a->d_workspace + q.product;
@@ -531,32 +530,23 @@ int check_loss_grad(const ec_loss_args *a) {
 }  // namespace
 
 uint64_t linear_cross_entropy_workspace_bytes(const ec_loss_args *a) {
-    if (check_loss(a)) return 0;
-    const LossArgs p = loss_args(a);
-    return loss_fits(p, false) ? loss_workspace(p) : 0;
+    uint64_t need;
+    return !check_loss(a) && loss_need(loss_args(a), &need) ? need : 0;
 }
 
 int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream) {
     const int rc = check_loss(a);
-    if (rc) return rc;
-    const LossArgs p = loss_args(a);
-    if (!loss_fits(p, false)) return EC_E_UNSUPPORTED;
-    const uint64_t need = loss_workspace(p);
-    if (need && (!a->d_workspace || a->workspace_bytes < need)) return EC_E_INVAL;
-    return hip_code(launch_loss(p, a->d_workspace, stream));
+    return rc ? rc : run_loss(loss_args(a), a->d_workspace, a->workspace_bytes, stream);
 }
 
 uint64_t linear_cross_entropy_grad_workspace_bytes(const ec_loss_args *a) {
-    return check_loss_grad(a) ? 0 : loss_grad_workspace(loss_args(a));
+    uint64_t need;
+    return !check_loss_grad(a) && loss_grad_need(loss_args(a), &need) ? need : 0;
 }
 
 int linear_cross_entropy_grad(const ec_loss_args *a, hipStream_t stream) {
     const int rc = check_loss_grad(a);
-    if (rc) return rc;
-    const LossArgs p = loss_args(a);
-    if (!loss_fits(p, true)) return EC_E_UNSUPPORTED;
-    if (!a->d_workspace || a->workspace_bytes < loss_grad_workspace(p)) return EC_E_INVAL;
-    return hip_code(launch_loss_grad(p, a->d_workspace, stream));
+    return rc ? rc : run_loss_grad(loss_args(a), a->d_workspace, a->workspace_bytes, stream);
 }
 
 // ----------------------------------------------------------------------- AdamW

@@ -77,7 +77,8 @@ struct ProductArgs {
     const float2 *row;                     // kOpLogitGrad: [I] log of the sum of exponentials, gradient of the loss
     const int32_t *row_target;             // kOpLogitGrad: [I] the target's column
     uint32_t first;                        // kOpLogitGrad: the piece's first column
-    const float *sum_in;                   // kOpPieceInput: added to D (as out in type and stride), or null
+    const float *sum_in;                   // kOpPieceInput: [I, J] added to D, or null
+    const uint32_t *kept;                  // kOpPieceInput: where D's rows go in out, or null
     // filled in by the plan
     uint32_t tiles_i, tiles_j, splits, blocks;
     float *partial;                        // [splits][tile][TI * TJ] when splits > 1
@@ -94,6 +95,7 @@ struct ColumnSumArgs {                     // db
 
 bool product_fits(const ProductArgs &a);            // whether some tile can address its rows
 uint64_t product_workspace(const ProductArgs &a);
+bool product_need(const ProductArgs &a, uint64_t *bytes);   // both, from one plan
 bool product_sums_columns(const ProductArgs &a);    // whether the product can write db as well
 hipError_t launch_product(ProductArgs a, void *workspace, hipStream_t s);
 hipError_t launch_check_offsets(const int32_t *offsets, uint32_t groups, uint32_t m, uint32_t *status, hipStream_t s);
@@ -142,11 +144,11 @@ struct LossArgs {
     uint32_t *status;
 };
 
-uint64_t loss_workspace(const LossArgs &a);
-uint64_t loss_grad_workspace(const LossArgs &a);
-bool loss_fits(const LossArgs &a, bool grad);
-hipError_t launch_loss(const LossArgs &a, void *workspace, hipStream_t s);
-hipError_t launch_loss_grad(const LossArgs &a, void *workspace, hipStream_t s);
+// The workspace's bytes, or false where sizes are too large; launches where the workspace given holds them.
+bool loss_need(const LossArgs &a, uint64_t *bytes);
+bool loss_grad_need(const LossArgs &a, uint64_t *bytes);
+int run_loss(const LossArgs &a, void *workspace, uint64_t bytes, hipStream_t s);        // ec_error
+int run_loss_grad(const LossArgs &a, void *workspace, uint64_t bytes, hipStream_t s);
 
 struct NormArgs {
     const void *x;
@@ -530,10 +532,11 @@ __device__ __forceinline__ void finish8(const ProductArgs &p, uint32_t g, uint32
     } else if constexpr (OP == kOpPieceInput) {
         if (p.sum_in) {
             float before[8];
-            load8(p.sum_in, EC_FP32, i * p.out_stride + j, c.left, before);
+            load8(p.sum_in, EC_FP32, (uint64_t)i * p.J + j, c.left, before);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] += before[q];
         }
+        if (p.kept) i = p.kept[i];
     } else if constexpr (OP == EC_LINEAR_GRAD_INPUT) {
         if constexpr (ACT != EC_ACT_NONE) {
             if (!zero) {

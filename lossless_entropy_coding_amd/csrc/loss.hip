@@ -9,7 +9,9 @@
 // second launch joins.  Backward: by pieces of the vocabulary the logits are
 // computed again, turned into G (bf16) in the epilogue, and multiplied with
 // the piece's weights (added up in fp32 over the pieces) and with the rows.
-// Rows without a target are left out of the backward pass before it begins.
+// Rows without a target are left out of the backward pass before it begins; the
+// last piece writes dx at the rows' own places (a launch of its own for that took
+// 4.8 us at 1023 x 1000 and 10.9 at 4096 x 2048, and one piece needs no fp32 sums).
 #include <string.h>
 
 #include "product_kernel.h"
@@ -85,34 +87,59 @@ __global__ __launch_bounds__(1024) void keep_rows_kernel(LossArgs p, int32_t *pl
     if (bad && p.status) __hip_atomic_fetch_or(p.status, EC_S_BAD_TARGET, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// x's kept rows one after the other, padded with zeros to 16 bytes, and what
-// the epilogue needs of each.
-__global__ __launch_bounds__(256) void gather_rows_kernel(LossArgs p, const uint32_t *kept, const uint32_t *used,
+// x's rows with a target one after the other, padded with zeros to 16 bytes,
+// with what the epilogues need of each; zeros in dx's other rows.  A wave takes
+// a row.  COUNT: a workgroup counts the rows with a target before its own (4096
+// rows: 16 KB from L2 on average) and keep_rows_kernel is not needed: 12.3 us at
+// 4096 x 2048, where the two launches took 5.6 + 8.4.
+template <bool COUNT>
+__global__ __launch_bounds__(256) void gather_rows_kernel(LossArgs p, const int32_t *place, uint32_t *kept, uint32_t *used,
                                                           uint16_t *x, uint32_t pitch, float2 *row, int32_t *row_target) {
-    const uint32_t chunks = pitch / 8 > 1 ? pitch / 8 : 1;          // a row of no columns has its target all the same
-    const uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x, r = q / chunks;
-    if (r >= *used) return;
-    const uint32_t i = kept[r], c = (uint32_t)(q - r * chunks) * 8;
-    if (c == 0) {
-        row[r] = float2{p.lse[i], p.dloss[p.dlosses > 1 ? i : 0]};
-        row_target[r] = (int32_t)target_at(p, i);
+    __shared__ uint32_t sh[4];
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = blockIdx.x * 4, i = first + wave;
+    const auto keeps = [&](uint32_t r) {
+        const int64_t t = target_at(p, r);
+        return t != p.ignore && t >= 0 && t < (int64_t)p.n;
+    };
+    bool keep = false;
+    int64_t target = 0;
+    if (i < p.m) {
+        target = target_at(p, i);
+        keep = target != p.ignore && target >= 0 && target < (int64_t)p.n;
     }
-    if (c >= p.k) return;
-    float v[8];
-    load8_bf16(p.x, i * p.x_stride + c, p.k - c, v);
-    store8(x, EC_BF16, r * pitch + c, 8, v);
-}
-
-// dx from the kept rows' sums; zeros in the others.
-__global__ __launch_bounds__(256) void scatter_rows_kernel(LossArgs p, const int32_t *place, const float *sum) {
-    const uint32_t chunks = (uint32_t)(((uint64_t)p.k + 7) / 8);
-    const uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x, i = q / chunks;
+    uint32_t at = 0;
+    if constexpr (COUNT) {
+        uint32_t n = 0;
+        for (uint32_t r = threadIdx.x; r < first; r += 256) n += keeps(r) ? 1 : 0;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) n += (uint32_t)__shfl_xor((int)n, d);
+        if (lane == 0) sh[wave] = n;
+        __syncthreads();
+        at = sh[0] + sh[1] + sh[2] + sh[3];
+        for (uint32_t r = first; r < i && r < p.m; ++r) at += keeps(r) ? 1 : 0;
+        if (lane == 0 && (i + 1 == p.m || (p.m == 0 && i == 0))) *used = at + (keep ? 1 : 0);
+        if (lane == 0 && i < p.m && !keep && target != p.ignore && p.status)
+            __hip_atomic_fetch_or(p.status, EC_S_BAD_TARGET, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    } else if (i < p.m && keep) {
+        at = (uint32_t)place[i];
+    }
     if (i >= p.m) return;
-    const uint32_t c = (uint32_t)(q - i * chunks) * 8, left = p.k - c;
-    const int32_t at = place[i];
-    float v[8] = {};
-    if (at >= 0) load8(sum, EC_FP32, (uint64_t)at * p.k + c, left, v);
-    store8(p.dx, EC_BF16, i * p.dx_stride + c, left, v);
+    if (keep) {
+        if (lane == 0) {
+            if constexpr (COUNT) kept[at] = i;
+            row[at] = float2{p.lse[i], p.dloss[p.dlosses > 1 ? i : 0]};
+            row_target[at] = (int32_t)target;
+        }
+        for (uint64_t c = lane * 8; c < p.k; c += 512) {
+            float v[8];
+            load8_bf16(p.x, i * p.x_stride + c, (uint32_t)(p.k - c), v);
+            store8(x, EC_BF16, (uint64_t)at * pitch + c, 8, v);
+        }
+    } else if (p.dx) {
+        const float v[8] = {};
+        for (uint64_t c = lane * 8; c < p.k; c += 512)
+            store8(p.dx, EC_BF16, i * p.dx_stride + c, (uint32_t)(p.k - c), v);
+    }
 }
 
 // ----------------------------------------------------------------- launches
@@ -126,8 +153,7 @@ void launch_tiles(const ProductArgs &a, const Plan &q, hipStream_t s) {
 }
 
 template <int OP>
-hipError_t launch_any(ProductArgs a, void *workspace, hipStream_t s) {
-    const Plan q = make_plan(a);
+hipError_t launch_planned(ProductArgs a, const Plan &q, void *workspace, hipStream_t s) {
     if (q.none) return hipErrorInvalidValue;
     const hipError_t e = place_product(a, q, workspace, s);
     if (e != hipSuccess) return e;
@@ -148,6 +174,11 @@ hipError_t launch_any(ProductArgs a, void *workspace, hipStream_t s) {
             }
     }
     return hipGetLastError();
+}
+
+template <int OP>
+hipError_t launch_any(const ProductArgs &a, void *workspace, hipStream_t s) {
+    return launch_planned<OP>(a, make_plan(a), workspace, s);
 }
 
 ProductArgs forward_product(const LossArgs &p) {
@@ -173,10 +204,12 @@ ProductArgs forward_product(const LossArgs &p) {
 // The pieces of the vocabulary and where the backward pass keeps what.
 constexpr uint64_t kPieceBytes = 512ull << 20;  // of G
 constexpr uint64_t kLeastPiece = 4096;
+// Rows whose place every workgroup of the gathering launch counts by itself.
+constexpr uint32_t kCountRows = 8192;
 
 struct Pieces {
     uint32_t columns, pitch, x_pitch, w_pitch;  // w_pitch: 0 where w is read in place
-    uint64_t place, kept, used, row, row_target, x, w, sum, g, product, bytes;
+    uint64_t place, kept, used, row, row_target, x, w, sum, g, product, bytes;     // place, sum: where needed
 };
 
 uint64_t take(uint64_t *at, uint64_t bytes) {
@@ -223,10 +256,17 @@ ProductArgs piece_product(const LossArgs &p, const Pieces &q, uint32_t op, uint3
         a.b = w;
         a.b_j = 1;
         a.b_c = w_stride;
-        a.out = ws + q.sum;
-        a.out_stride = p.k;
-        a.out_dtype = EC_FP32;
         a.sum_in = first ? (const float *)(ws + q.sum) : nullptr;
+        if (p.n - first <= q.columns) {     // the last piece
+            a.out = p.dx;
+            a.out_stride = p.dx_stride;
+            a.out_dtype = EC_BF16;
+            a.kept = (const uint32_t *)(ws + q.kept);
+        } else {
+            a.out = ws + q.sum;
+            a.out_stride = p.k;
+            a.out_dtype = EC_FP32;
+        }
     } else {
         a.I = columns;
         a.J = p.k;
@@ -270,73 +310,80 @@ bool lay_out(const LossArgs &p, Pieces *q) {
     const bool in_place = !((((uintptr_t)p.w | p.w_stride * 2) & 15) || (p.k & 7));
     q->w_pitch = in_place ? 0 : (uint32_t)pitch;
     uint64_t at = 0;
-    q->place = take(&at, (uint64_t)p.m * 4);
+    q->place = take(&at, p.m > kCountRows ? (uint64_t)p.m * 4 : 0);
     q->kept = take(&at, (uint64_t)p.m * 4);
     q->used = take(&at, 4);
     q->row = take(&at, (uint64_t)p.m * 8);
     q->row_target = take(&at, (uint64_t)p.m * 4);
     q->x = take(&at, p.m * pitch * 2);
     q->w = take(&at, q->w_pitch ? q->columns * pitch * 2 : 0);
-    q->sum = take(&at, p.dx ? (uint64_t)p.m * p.k * 4 : 0);
+    q->sum = take(&at, p.dx && q->columns < p.n ? (uint64_t)p.m * p.k * 4 : 0);
     q->g = take(&at, (uint64_t)p.m * q->pitch * 2);
     q->product = at;
     const uint32_t last = (p.n - 1) / q->columns * q->columns;
-    uint64_t whole, rest;
-    if (!products_fit(p, *q, 0, &whole) || !products_fit(p, *q, last, &rest)) return false;
+    uint64_t whole, rest = 0;
+    if (!products_fit(p, *q, 0, &whole) || (last && !products_fit(p, *q, last, &rest))) return false;
     q->bytes = at + (whole > rest ? whole : rest);
-    // the gathering and scattering launches
-    const uint64_t chunks = pitch / 8 > 1 ? pitch / 8 : 1;
-    return launchable(ceil_div(p.m * chunks, 256), 256) && launchable(ceil_div(q->columns * chunks, 256), 256);
+    // the launches that gather rows and copy w
+    return launchable(ceil_div(p.m, 4), 256) && launchable(ceil_div(q->columns * (pitch / 8), 256), 256);
 }
 
 }  // namespace
 
-bool loss_fits(const LossArgs &a, bool grad) {
-    if (grad) {
-        Pieces q;
-        return lay_out(a, &q);
-    }
-    return !a.m || (!make_plan(forward_product(a)).none && launchable(a.m, 256));
+static bool forward_need(const LossArgs &p, const Plan &q, uint64_t *bytes) {
+    *bytes = round_up(q.bytes, 256) + round_up((uint64_t)p.m * q.tiles_j * 8, 256) + (uint64_t)p.m * 4;
+    return !q.none && launchable(p.m, 256);
 }
 
-uint64_t loss_workspace(const LossArgs &a) {
-    if (!a.m) return 0;
-    const Plan q = make_plan(forward_product(a));
-    return round_up(q.bytes, 256) + round_up((uint64_t)a.m * q.tiles_j * 8, 256) + (uint64_t)a.m * 4;
+bool loss_need(const LossArgs &p, uint64_t *bytes) {
+    *bytes = 0;
+    return !p.m || forward_need(p, make_plan(forward_product(p)), bytes);
 }
 
-uint64_t loss_grad_workspace(const LossArgs &a) {
+bool loss_grad_need(const LossArgs &p, uint64_t *bytes) {
     Pieces q;
-    return lay_out(a, &q) ? q.bytes : 0;
+    *bytes = 0;
+    if (!lay_out(p, &q)) return false;
+    *bytes = q.bytes;
+    return true;
 }
 
-hipError_t launch_loss(const LossArgs &p, void *workspace, hipStream_t s) {
-    if (!p.m) return hipSuccess;
+int run_loss(const LossArgs &p, void *workspace, uint64_t bytes, hipStream_t s) {
+    if (!p.m) return EC_OK;
     ProductArgs a = forward_product(p);
     const Plan q = make_plan(a);
+    uint64_t need;
+    if (!forward_need(p, q, &need)) return EC_E_UNSUPPORTED;
+    if (!workspace || bytes < need) return EC_E_INVAL;
     char *ws = (char *)workspace;
     a.stats = (float2 *)(ws + round_up(q.bytes, 256));
     a.hit = (float *)((char *)a.stats + round_up((uint64_t)p.m * q.tiles_j * 8, 256));
-    const hipError_t e = launch_any<kOpRowStats>(a, workspace, s);
-    if (e != hipSuccess) return e;
+    const hipError_t e = launch_planned<kOpRowStats>(a, q, workspace, s);
+    if (e != hipSuccess) return EC_E_HIP;
     if (p.m > 1024)
         join_stats_kernel<64><<<(p.m + 3) / 4, 256, 0, s>>>(p, a.stats, a.hit, q.tiles_j);
     else
         join_stats_kernel<256><<<p.m, 256, 0, s>>>(p, a.stats, a.hit, q.tiles_j);
-    return hipGetLastError();
+    return hipGetLastError() == hipSuccess ? EC_OK : EC_E_HIP;
 }
 
-hipError_t launch_loss_grad(const LossArgs &p, void *workspace, hipStream_t s) {
+int run_loss_grad(const LossArgs &p, void *workspace, uint64_t bytes, hipStream_t s) {
     Pieces q;
-    if (!lay_out(p, &q)) return hipErrorInvalidValue;
+    if (!lay_out(p, &q)) return EC_E_UNSUPPORTED;
+    if (!workspace || bytes < q.bytes) return EC_E_INVAL;
     char *ws = (char *)workspace;
     int32_t *place = (int32_t *)(ws + q.place);
     uint32_t *kept = (uint32_t *)(ws + q.kept), *used = (uint32_t *)(ws + q.used);
-    keep_rows_kernel<<<1, 1024, 0, s>>>(p, place, kept, used);
-    const uint64_t chunks = q.x_pitch / 8 > 1 ? q.x_pitch / 8 : 1;
-    if (p.m)
-        gather_rows_kernel<<<(uint32_t)ceil_div(p.m * chunks, 256), 256, 0, s>>>(
-            p, kept, used, (uint16_t *)(ws + q.x), q.x_pitch, (float2 *)(ws + q.row), (int32_t *)(ws + q.row_target));
+    const auto gather = [&](auto kernel) {
+        kernel<<<p.m > 4 ? (p.m + 3) / 4 : 1, 256, 0, s>>>(p, place, kept, used, (uint16_t *)(ws + q.x), q.x_pitch,
+                                                          (float2 *)(ws + q.row), (int32_t *)(ws + q.row_target));
+    };
+    if (p.m > kCountRows) {
+        keep_rows_kernel<<<1, 1024, 0, s>>>(p, place, kept, used);
+        gather(gather_rows_kernel<false>);
+    } else {
+        gather(gather_rows_kernel<true>);
+    }
     hipError_t e = hipGetLastError();
     for (uint32_t first = 0; e == hipSuccess && p.k && (p.dx || p.dw); first += q.columns) {
         const uint32_t columns = p.n - first < q.columns ? p.n - first : q.columns;
@@ -350,12 +397,7 @@ hipError_t launch_loss_grad(const LossArgs &p, void *workspace, hipStream_t s) {
             e = launch_any<kOpPieceWeight>(piece_product(p, q, kOpPieceWeight, first, ws), ws + q.product, s);
         if (p.n - first <= q.columns) break;
     }
-    if (e == hipSuccess && p.dx && p.m && p.k) {
-        scatter_rows_kernel<<<(uint32_t)ceil_div((uint64_t)p.m * ceil_div(p.k, 8), 256), 256, 0, s>>>(
-            p, place, (const float *)(ws + q.sum));
-        e = hipGetLastError();
-    }
-    return e;
+    return e == hipSuccess ? EC_OK : EC_E_HIP;
 }
 
 }  // namespace ec

@@ -339,6 +339,14 @@ bool product_sums_columns(const ProductArgs &a) {
 
 bool product_fits(const ProductArgs &a) { return !a.I || !a.J || !make_plan(a).none; }
 
+bool product_need(const ProductArgs &a, uint64_t *bytes) {
+    *bytes = 0;
+    if (!a.I || !a.J) return true;
+    const Plan q = make_plan(a);
+    *bytes = q.bytes;
+    return !q.none;
+}
+
 uint64_t product_workspace(const ProductArgs &a) {
     if (!a.I || !a.J) return 0;
     return make_plan(a).bytes;

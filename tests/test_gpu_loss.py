@@ -49,20 +49,20 @@ def test_forward_and_backward(ec, size):
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
-def test_several_pieces(ec):
-    """A vocabulary of more than one piece (40000 rows: 6656 entries, then the rest)."""
-    m, k, n = 40000, 16, 9001
+@pytest.mark.parametrize("m,k,n,piece", [(40000, 16, 9001, 6656), (8000, 24, 40001, 33536)])
+def test_several_pieces(ec, m, k, n, piece):
+    """A vocabulary of more than one piece (512 MiB of the logits' gradient, in whole 256 entries)."""
     x, w, t, dl = _inputs(m, k, n, 3)
     loss, lse = ec.linear_cross_entropy(x, w, t)
     dx, dw = ec.linear_cross_entropy_backward(dl, x, w, t, lse, dw_dtype=torch.float32)
-    part = slice(0, None, 401)
+    part = slice(0, None, 101)
     want, tol, want_lse, tol_lse, _, _ = tr.loss(x[part], w, t[part])
     near(loss[part], want, tol, "loss")
     near(lse[part], want_lse, tol_lse, "lse")
     (wx, tx), _ = tr.loss_backward(dl[part], x[part], w, t[part])
     near(dx[part], wx, tx, "dx")
     # every row's share in dw, for some entries of each piece
-    sel = torch.tensor([0, 1, 4095, 6655, 6656, 8192, 9000], device="cuda")
+    sel = torch.tensor([0, 1, 4095, piece - 1, piece, piece + 255, n - 1], device="cuda")
     l = tr.mm(x.double(), w[sel].double())
     G = torch.exp(l - lse.double()[:, None])
     G -= (t[:, None] == sel[None, :]).double()
