@@ -761,7 +761,9 @@ int linear_cross_entropy_grad(const ec_loss_args *a, hipStream_t stream);
  * 2^-60 at least, that take the block's values to at most 448.  Both are
  * rounded up or down at random so that their means are kept, by bits that are
  * a function of seed, t and the value's place.  Values that are not finite
- * become NaN.
+ * become NaN.  In p's change sqrt(v) is then at least sqrt(beta2) 2^-9
+ * v_scale[block] (the scale before the step), what the least v that can be held
+ * leaves: a v held as 0 is below that, but by how much is not known.
  * ------------------------------------------------------------------------- */
 #define EC_ADAMW_BLOCK 256
 

@@ -16,6 +16,14 @@
 // of each come from a hash of (seed, step, place), so that the same call gives
 // the same bits.
 //
+// A v held as 0 says only that it was below the least square of its block, the
+// square of 2^-9 scales, while the m beside it may be held as a whole step: m /
+// sqrt(v) would then be anything (hundreds of lr where a value's gradients are
+// 1e-5 of its block's largest or less; those of exact states are within 7.3 of 0
+// with b1 = 0.9, b2 = 0.999).  The change of p therefore takes sqrt(b2) times
+// that least root where v's own is below it: at least what any v held as more
+// than 0 leaves, and never less than what v stood for.  v itself stays as it is.
+//
 // Bound by HBM: one pass, 28 bytes a value with fp32 states, bf16 gradients and
 // a bf16 copy, 16 with e4m3 states.
 #include "ffn_common.h"
@@ -126,6 +134,7 @@ __device__ __forceinline__ uint32_t maxima(const uint32_t (&v)[8]) {
 // What a step's formulas take besides the tensors.
 struct Step {
     float scale, rate, widen, keep;         // keep: 1 - lr decay, of the tensor
+    float least;                            // e4m3: v's root at the least, over its block's scale
     uint32_t key;
 };
 
@@ -196,13 +205,16 @@ __device__ __forceinline__ void step_blocks(const AdamArgs &a, const AdamTensor 
                 v[k][q] = root * root;
             }
         }
+        const float least = E4M3 ? vs[k] * c.least : 0.0f;
         float most[2] = {0.0f, 0.0f};       // without NaN
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float d = g[k][q] * c.scale;
             m[k][q] = m[k][q] * a.b1 + d * a.rest1;
             v[k][q] = v[k][q] * a.b2 + (d * d) * a.rest2;
-            const float below = root_of(v[k][q]) * c.widen + a.eps;
+            float root = root_of(v[k][q]);
+            if constexpr (E4M3) root = root < least ? least : root;         // NaN stays
+            const float below = root * c.widen + a.eps;
             p[k][q] = p[k][q] * c.keep - c.rate * m[k][q] * __builtin_amdgcn_rcpf(below);
             most[0] = fmaxf(most[0], fabsf(m[k][q]));
             most[1] = fmaxf(most[1], v[k][q]);
@@ -303,6 +315,7 @@ __global__ __launch_bounds__(WAVES * 64) void adamw_kernel(AdamPart part) {
     const float lr = a.lr_at ? *a.lr_at : a.lr;
     c.rate = lr / one_minus_exp((float)now * a.log_b1);
     c.widen = 1.0f / sqrtf(one_minus_exp((float)now * a.log_b2));
+    c.least = sqrtf(a.b2) * 0x1p-9f;
     c.key = mix((uint32_t)now ^ mix(a.seed));
     if constexpr (ALONE) {
         __syncthreads();                    // every wave has the number

@@ -234,7 +234,9 @@ def adamw(params, grads, state: AdamWState, *, lr=1e-3, betas=(0.9, 0.999), eps=
     States in e4m3 are rounded up or down at random, so that their means are
     kept: by a function of seed (32 bits), the step's number and the place, so
     that the same call gives the same bits.  Values that are not finite become
-    NaN there.  No two tensors may overlap."""
+    NaN there.  Where v is held as 0 beside much larger values of its block, the
+    step takes the least root that can be held (2^-9 v_scale), so that such a
+    value moves by a few lr at most.  No two tensors may overlap."""
     if not isinstance(params, (list, tuple)) or not params or not isinstance(params[0], torch.Tensor) or not params[0].is_cuda:
         _params(params)
     if stream is not None and stream.device != params[0].device:
