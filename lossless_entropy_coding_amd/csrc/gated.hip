@@ -112,7 +112,7 @@ void launch_few(const ProductArgs &a, const Plan &q, hipStream_t s) {
     if (q.row_tiles == 2)
         q.waves == 4 ? few_gated_kernel<2, 4, E4M3, false><<<n, 256, 0, s>>>(a)
                      : few_gated_kernel<2, 8, E4M3, false><<<n, 512, 0, s>>>(a);
-    else if (!a.groups && a.I <= kSplitRows && n >= kSplitBlocks)
+    else if (!a.groups && a.I <= kSplitRows && n >= kSplitBlocks && launchable(n, 512))     // the plan counted 256
         few_gated_kernel<1, 8, E4M3, true><<<n, 512, 0, s>>>(a);
     else
         q.waves == 4 ? few_gated_kernel<1, 4, E4M3, false><<<n, 256, 0, s>>>(a)
