@@ -360,26 +360,15 @@ hipError_t AdamBatch::launch(bool alone) {
     return hipGetLastError();
 }
 
-hipError_t AdamBatch::add(AdamTensor t) {
-    constexpr uint32_t kMost = 1u << 31;    // chunks a launch
-    while (t.n) {                           // a tensor of more than a launch's chunks is cut at a block
-        if (part.count == kAdamTensors || part.chunks == kMost) {
-            const hipError_t e = launch(false);
-            if (e != hipSuccess) return e;
-        }
-        const uint64_t chunks = (adamw_blocks(t.n) + kPerWave - 1) / kPerWave, room = kMost - part.chunks;
-        const uint64_t now = chunks < room ? chunks : room, values = now * kPerWave * kBlock;
-        AdamTensor &to = part.t[part.count];
-        to = t;
-        if (to.n > values) to.n = values;
-        part.first[part.count++] = part.chunks;
-        part.chunks += (uint32_t)now;
-        t.p += to.n;
-        t.g = (const char *)t.g + to.n * (t.grad_bf16 ? 2 : 4);
-        if (t.copy) t.copy += to.n;
-        t.block += now * kPerWave;
-        t.n -= to.n;
+hipError_t AdamBatch::add(const AdamTensor &t) {
+    if (!t.n) return hipSuccess;
+    if (part.count == kAdamTensors) {
+        const hipError_t e = launch(false);
+        if (e != hipSuccess) return e;
     }
+    part.t[part.count] = t;
+    part.first[part.count++] = part.chunks;
+    part.chunks += (uint32_t)((adamw_blocks(t.n) + kPerWave - 1) / kPerWave);
     return hipSuccess;
 }
 

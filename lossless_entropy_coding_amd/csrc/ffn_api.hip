@@ -568,6 +568,7 @@ int adamw_step(const ec_adamw_tensor *tensors, uint32_t count, const ec_adamw_ar
         if (((uintptr_t)t.d_param & 3) || ((uintptr_t)t.d_grad & (t.grad_dtype == EC_BF16 ? 1 : 3)) || ((uintptr_t)t.d_copy & 1))
             return EC_E_INVAL;
         blocks += adamw_blocks(t.n);
+        if (blocks > kAdamBlocks) return EC_E_UNSUPPORTED;
     }
     if (blocks > a->state_blocks) return EC_E_INVAL;
     if (blocks && (!a->d_m || !a->d_v || (((uintptr_t)a->d_m | (uintptr_t)a->d_v) & 15))) return EC_E_INVAL;

@@ -7,6 +7,9 @@
 namespace ec {
 
 constexpr uint32_t kAdamTensors = 56;       // a launch's, in its arguments
+// State blocks of a step, more than a card's memory holds: a launch's chunks of
+// four blocks, at most one begun a tensor, are then counted in 32 bits.
+constexpr uint64_t kAdamBlocks = 1ull << 32;
 
 struct AdamTensor {
     float *p;
@@ -45,7 +48,7 @@ struct AdamBatch {
         part.a = a;
         part.count = part.chunks = 0;
     }
-    hipError_t add(AdamTensor t);
+    hipError_t add(const AdamTensor &t);
     hipError_t launch(bool alone);           // alone: the only launch of the step
     hipError_t finish();                    // the last launch, and the step's number
 };
