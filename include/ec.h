@@ -728,7 +728,8 @@ typedef struct ec_loss_args {
 /*
  * lse[m]  = log sum_v exp(l[m, v])
  * loss[m] = lse[m] - l[m, target[m]]
- * Products and sums in fp32.  m up to 2^24 - 1 (EC_E_UNSUPPORTED beyond).
+ * Products and sums in fp32.  loss is computed from the row's maximum, not from
+ * the rounded lse, and never negative.  m up to 2^24 - 1 (EC_E_UNSUPPORTED beyond).
  */
 uint64_t linear_cross_entropy_workspace_bytes(const ec_loss_args *a);
 int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream);
@@ -739,7 +740,9 @@ int linear_cross_entropy(const ec_loss_args *a, hipStream_t stream);
  *   dw[v, k] = sum_m G[m, v] x[m, k]        (dw_dtype)
  * The logits are computed again by pieces of the vocabulary; a piece's G is
  * rounded to bf16 for the products and lies in the workspace (512 MiB, or 8 KiB
- * a row where that is more), beside x and the fp32 sums of dx.  Fixed order of
+ * a row where that is more), beside x and the fp32 sums of dx.  lse's rounding,
+ * 2^-24 of it, is an error of the same size of every exp(l - lse), below that of
+ * bf16 except in the target's own G of a row that is nearly sure.  Fixed order of
  * summation.  m up to 2^26 - 4, k up to 2^24 - 1024 (EC_E_UNSUPPORTED beyond).
  * Outputs overlap nothing that is read.
  */

@@ -44,11 +44,14 @@ __global__ __launch_bounds__(256) void join_stats_kernel(LossArgs p, const float
         s = join_stats(join_stats(sh[0], sh[1]), join_stats(sh[2], sh[3]));
     }
     if (t) return;
-    const float lse = s.x + logf(s.y);      // -inf where every logit is
+    const float rest = logf(s.y), lse = s.x + rest;     // -inf where every logit is
     if (p.lse) p.lse[i] = lse;
     const int64_t target = target_at(p, i);
     const bool out = target != p.ignore && (target < 0 || target >= (int64_t)p.n);
-    p.loss[i] = target == p.ignore || out ? 0.0f : lse - hit[i];
+    // From the maximum and not from lse, whose rounding may be more than a sure
+    // row's whole loss (2^-24 of lse, that is 5e-4 at logits of 8192).  Neither
+    // part is negative.
+    p.loss[i] = target == p.ignore || out ? 0.0f : rest + (s.x - hit[i]);
     if (out && p.status) __hip_atomic_fetch_or(p.status, EC_S_BAD_TARGET, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
