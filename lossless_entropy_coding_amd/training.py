@@ -212,6 +212,13 @@ def _float_bits(v: float) -> int:
     return struct.unpack("<I", struct.pack("<f", v))[0]
 
 
+def _once(places, sizes, name: str):
+    """Refuses a tensor that is listed twice (tied weights): two writers of one place."""
+    held = [p for p, n in zip(places, sizes) if p and n]
+    if len(set(held)) != len(held):
+        _error("%s must not hold the same tensor twice (tied weights are listed once, with the sum of their gradients)" % name)
+
+
 def _bad_param(p, dev):
     _params([p])
     _error("params are on %s and %s" % (dev, p.device))
@@ -281,6 +288,9 @@ def adamw(params, grads, state: AdamWState, *, lr=1e-3, betas=(0.9, 0.999), eps=
             copy = c.data_ptr()
         words += (p.data_ptr(), g.data_ptr(), copy, n, decay)
         blocks += (n + 255) >> 8
+    if len(set(words[::5])) != count or copies is not None:
+        _once(words[::5], words[3::5], "params")
+        _once(words[2::5], words[3::5], "copies")
     if not isinstance(state, (list, tuple)) or len(state) != 5:
         _error("state must be an AdamWState")
     m, v, m_scale, v_scale, steps = state
