@@ -161,7 +161,12 @@ hipError_t launch_planned(ProductArgs a, const Plan &q, void *workspace, hipStre
     const hipError_t e = place_product(a, q, workspace, s);
     if (e != hipSuccess) return e;
     switch (q.shape) {
-        case kHuge: runs_wide(a, q) ? launch_wide<OP, EC_ACT_NONE>(a, q, s) : launch_tiles<Huge, OP>(a, q, s); break;
+        case kHuge:
+            if constexpr (OP == kOpRowStats)                // always Wide's
+                launch_wide<OP, EC_ACT_NONE>(a, q, s);
+            else
+                runs_wide(a, q) ? launch_wide<OP, EC_ACT_NONE>(a, q, s) : launch_tiles<Huge, OP>(a, q, s);
+            break;
         case kEven: launch_tiles<Even, OP>(a, q, s); break;
         case kSmall: launch_tiles<Small, OP>(a, q, s); break;
         case kTall: launch_tiles<Tall, OP>(a, q, s); break;
