@@ -320,12 +320,13 @@ __device__ __forceinline__ GatedColumns load_gated_columns(const ProductArgs &p,
     c.left = p.J > j ? p.J - j : 0;
     const uint64_t at = (uint64_t)g * 2 * p.J + j;
     if (p.w_scale) {
+        // not in a branch of its own, for which the compiler keeps the address in scratch memory
+        const float one = p.w_scale[p.w_scales > 1 ? (uint64_t)g * 2 * p.J : g];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) c.gate.w_scale[q] = c.rest.w_scale[q] = one;
         if (p.w_scales > 1) {
             load8(p.w_scale, EC_FP32, at, c.left, c.gate.w_scale);
             load8(p.w_scale, EC_FP32, at + p.J, c.left, c.rest.w_scale);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) c.gate.w_scale[q] = c.rest.w_scale[q] = p.w_scale[g];
         }
     }
     if (p.bias) {
