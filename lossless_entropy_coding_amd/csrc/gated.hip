@@ -10,13 +10,19 @@ namespace {
 // As few_rows_kernel, with the 16 columns' rows of the gate and of the factor
 // beside it.  A wave takes both, or (SPLIT) half of the waves one and half the
 // other: then a lane has eight loads of one stretch of memory on the way and
-// not four of each of two.  One row by 2 x 16384 x 2048 bf16 weights: 28.5 us
-// split over eight waves (4.7 TB/s), 31.4 over four, 33.8 not split.  Where
-// workgroups are few or have more rows the loads of A weigh more: 4 rows by 2 x
-// 2048 x 8192 26 us split, 22.9 not; 16 by 2 x 8192 x 2048 19.6 and 17.6; 17 by
-// 2 x 16384 x 2048 46 and 42; 64 rows over 32 experts of 2 x 1024 x 2048 in
-// e4m3 34 and 28.8.
-constexpr uint32_t kSplitBlocks = 512, kSplitRows = 4;
+// not four of each of two.  By 2 x 16384 x 2048 bf16 weights, split over eight
+// waves and not (us): one row 31.3 and 33.9, four 32.7 and 35.0; one by 2 x 8192
+// x 8192 70 and 78.  The rule's borders, split and not:
+// rows: eight by 2 x 16384 x 2048 34.4 and 35.4, x 1024 16.6 and 15.2; 16 rows
+// x 2048 39.6 and 37.6, 17 46 and 42, where the loads of A weigh more; 64 rows over
+// 32 experts of 2 x 1024 x 2048 in e4m3 34 and 28.8;
+// workgroups: one row by 2 x 4096 x 8192 (256 of them) 38.5 and 32.9, 2 x 6144 x
+// 8192 (384) 56.6 and 53.9, 2 x 8192 x 2048 (512) 14.9 and 15.7;
+// bytes of a row, of which a wave has a quarter: one row by 2 x 16384 e4m3 rows
+// of 2048 18.0 and 15.7, 4096 32.6 and 32.4, 8192 63 and 66; by 2 x 28672, 1024
+// 17.4 and 14.9, 2048 29.5 and 28.8, 4096 51.0 and 52.7.  bf16 rows of 2048 bytes
+// gain (2 x 28672: 28.5 and 29.5): they have half the conversions.
+constexpr uint32_t kSplitBlocks = 512, kSplitRows = 4, kSplitLength = 4096;     // kSplitLength: of e4m3 rows
 
 template <int RT>
 struct FewGated {
@@ -112,7 +118,8 @@ void launch_few(const ProductArgs &a, const Plan &q, hipStream_t s) {
     if (q.row_tiles == 2)
         q.waves == 4 ? few_gated_kernel<2, 4, E4M3, false><<<n, 256, 0, s>>>(a)
                      : few_gated_kernel<2, 8, E4M3, false><<<n, 512, 0, s>>>(a);
-    else if (!a.groups && a.I <= kSplitRows && n >= kSplitBlocks && launchable(n, 512))     // the plan counted 256
+    else if (!a.groups && a.I <= kSplitRows && n >= kSplitBlocks && (!E4M3 || a.C >= kSplitLength) &&
+             launchable(n, 512))            // the plan counted 256
         few_gated_kernel<1, 8, E4M3, true><<<n, 512, 0, s>>>(a);
     else
         q.waves == 4 ? few_gated_kernel<1, 4, E4M3, false><<<n, 256, 0, s>>>(a)

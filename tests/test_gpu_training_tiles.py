@@ -198,10 +198,11 @@ def test_rows_without_a_target(ec, m):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-@pytest.mark.parametrize("k", [1, 31, 77, 2050])
+@pytest.mark.parametrize("k", [1, 31, 77, 2050, 4095, 4096, 4111])
 @pytest.mark.parametrize("m", [1, 2, 4, 5])
 def test_gated_few_rows_many_columns(ec, m, k, kind):
-    """Up to four rows by 512 and more workgroups' columns share the waves by half; lengths that end inside a load."""
+    """Up to four rows by 512 and more workgroups' columns share the waves by half (in e4m3 from 4096
+    values on); lengths that end inside a load."""
     n = 8200
     g = torch.Generator(device="cuda").manual_seed(m * k)
     if kind == "bf16":
