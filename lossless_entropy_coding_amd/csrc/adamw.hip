@@ -39,8 +39,9 @@ constexpr int kWaves = 4, kAloneWaves = 16; // a workgroup's
 // million values with fp32 states: 185 us with 4096, 180 with 8192, 186 with
 // 16384.
 constexpr uint32_t kMostBlocks = 8192;
-// Chunks up to which one workgroup does a step alone, the step's number too,
-// which otherwise is a launch of its own: 7 us for 18 chunks, 7 and 5 so.
+// Chunks up to which one workgroup does a step alone, and moves the step's number
+// on, which takes a launch of its own after several workgroups.  18 chunks: 7 us
+// alone; in several workgroups 7 us and 5 for the number.
 constexpr uint32_t kAloneChunks = 32;
 
 // At any address that suits their elements.  Params and states are read and

@@ -123,9 +123,12 @@ __global__ __launch_bounds__(64) void check_offsets_kernel(const int32_t *offset
 // What a plan's time is made of, measured on whole runs (us): a stage of one
 // workgroup alone on its CU, a stage per workgroup where every CU is full, and
 // what a workgroup costs besides its stages; bf16 and e4m3.  The full rates
-// are 1.25, 0.87, 0.51 and 1.17 PFLOP/s in bf16.  The last, of 129 to 256 rows
-// in a row of as many workgroups as CUs: 160 x 32768 x 2048 maxima and sums 40 us,
-// 46.7 in tiles of 128 x 128; 160 x 2 x 16384 x 2048 gated 36 and 43.
+// are 1.25, 0.87, 0.51 and 1.17 PFLOP/s in bf16.  The last is for 129 to 256
+// rows in a row of as many workgroups as CUs; whole calls with it and without
+// (us): the loss of M rows x 32768 x 2048, M = 129 50.9 and 53.7, 160 52.4 and
+// 55.4, 256 57.6 and 59.7, 320 67.1 and 66.7; gated M x 2 x 16384 x 2048 48.8 and
+// 58.5, 50.0 and 59.8, 57.5 and 64.7, 70.5 and 70.2.  ec_linear_op's products do
+// not have it: what they ran in before keeps its times.
 struct ShapeCost {
     uint32_t TI, TJ, threads, per_cu;
     float alone[2], full[2], fixed;

@@ -1343,12 +1343,15 @@ hipError_t place_product(ProductArgs &a, const Plan &q, void *workspace, hipStre
 namespace {
 
 // Whether the tiles of 256 x 256 are Wide's: where the contraction of a
-// workgroup is long, since four waves take longer for what surrounds it.  50001
-// x 920 x 1000: 147 us so and 124 by eight waves (weight gradient); 32768 x 3690
-// x 2048: 421 and 431.  An epilogue that stores nothing does not weigh: maxima and
-// sums of 1023 x 50001 x 1000 logits 152 and 164 us, 4096 x 131072 x 2048 1902
-// and 2027.  Where the contraction is outermost a stage's 64 rows must be within
-// 2 GiB, twice what the other tiles' 32 need.
+// workgroup is long, since four waves take longer for what surrounds it.  Gated
+// 2048 x 2 x 16384 by a contraction of 1024 165.5 us so and 158.5 by eight
+// waves, 1280 191.9 and 191.5, 1536 212.5 and 218.9, 2048 260.6 and 268.4; loss
+// with gradients of M x 65536 x 2048, where M is the weight gradient's: 1024
+// 1015 and 990, 1536 1551 and 1542, 2048 1835 and 1843.  An epilogue that stores
+// nothing does not weigh: maxima and sums of 1023 x 50001 x 1000 logits 152 and
+// 164 us, 4096 x 131072 x 2048 1902 and 2027.  Where the contraction is outermost
+// a stage's 64 rows must be within 2 GiB, twice what the other tiles' 32 need.
+// The plan's costs are those of the eight waves: it chooses the tiles, not these.
 inline bool runs_wide(const ProductArgs &a, const Plan &q) {
     const uint32_t parts = contracts_a_rows(a.op) && a.groups ? a.groups : q.splits;
     const auto far = [](uint64_t stride) { return Wide::kDepth * stride * 2 + 65536 >= 1ull << 31; };
