@@ -1188,24 +1188,6 @@ __device__ __forceinline__ void few_multiply(f32x4 (&acc)[RT], const u32x4 &b, c
     }
 }
 
-template <int RT, int ACT>
-__device__ __forceinline__ void few_finish(const ProductArgs &p, const Place &q, const float *sums, uint32_t waves) {
-    const uint32_t t = threadIdx.x, i = q.i0 + (t >> 1), j = q.j0 + (t & 1) * 8;
-    if (t >= RT * 32 || i >= q.i1) return;
-    const Columns c = load_columns<EC_LINEAR_FORWARD>(p, q.group, j);
-    float side[8], v[8] = {};
-    load_side<EC_LINEAR_FORWARD>(p, i, j, c.left, side);
-    const float xs = p.x_scale ? p.x_scale[p.x_scales > 1 ? i : 0] : 1.0f, os = p.out_scale ? *p.out_scale : 1.0f;
-    for (uint32_t w = 0; w < waves; ++w)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f32x4 s = *(const f32x4 *)(sums + (w * (RT * 16) + (t >> 1)) * 20 + (t & 1) * 8 + h * 4);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[4 * h + r] += s[r];
-        }
-    finish8<EC_LINEAR_FORWARD, ACT>(p, q.group, i, j, v, c, side, xs, os, q.zero);
-}
-
 // The eight sums of a thread's row and columns, over the waves in their order.
 template <int RT>
 __device__ __forceinline__ void few_sums(const float *sums, uint32_t waves, float *v) {
@@ -1217,6 +1199,18 @@ __device__ __forceinline__ void few_sums(const float *sums, uint32_t waves, floa
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[4 * h + r] += s[r];
         }
+}
+
+template <int RT, int ACT>
+__device__ __forceinline__ void few_finish(const ProductArgs &p, const Place &q, const float *sums, uint32_t waves) {
+    const uint32_t t = threadIdx.x, i = q.i0 + (t >> 1), j = q.j0 + (t & 1) * 8;
+    if (t >= RT * 32 || i >= q.i1) return;
+    const Columns c = load_columns<EC_LINEAR_FORWARD>(p, q.group, j);
+    float side[8], v[8] = {};
+    load_side<EC_LINEAR_FORWARD>(p, i, j, c.left, side);
+    const float xs = p.x_scale ? p.x_scale[p.x_scales > 1 ? i : 0] : 1.0f, os = p.out_scale ? *p.out_scale : 1.0f;
+    few_sums<RT>(sums, waves, v);
+    finish8<EC_LINEAR_FORWARD, ACT>(p, q.group, i, j, v, c, side, xs, os, q.zero);
 }
 
 template <int RT>

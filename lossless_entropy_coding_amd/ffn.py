@@ -159,14 +159,19 @@ def _warn_unrecorded(level: int, *tensors):
                 return
 
 
-def _call(name: str, args: _LinearArgs, op: int, device):
+def _run(size: str, name: str, args, device, *kind):
+    """A call of the library whose workspace another function of it, `size`, tells (of the `kind` of call)."""
     ec = _ec()
     L = ec.lib()
-    need = int(L.linear_workspace_bytes(ctypes.byref(args), op))
+    need = int(getattr(L, size)(ctypes.byref(args), *kind))
     if need:  # freed at return, to be used again in the order of this stream
         ws = _empty(need, torch.uint8, device)
         args.workspace, args.workspace_bytes = ws.data_ptr(), need
     ec._check(getattr(L, name)(ctypes.byref(args), ec._stream(None)), name)
+
+
+def _call(name: str, args: _LinearArgs, op: int, device):
+    _run("linear_workspace_bytes", name, args, device, op)
 
 
 def _weights(w, name: str, offsets, dtypes):
@@ -432,17 +437,6 @@ def _gated(x, w, offsets, bias, act, x_scale, w_scale, out_scale, out_dtype, sav
     return out if preact is None else (out, preact)
 
 
-def _run(size: str, name: str, args, device):
-    """A call whose workspace another function of the library tells."""
-    ec = _ec()
-    L = ec.lib()
-    need = int(getattr(L, size)(ctypes.byref(args)))
-    if need:  # freed at return, to be used again in the order of this stream
-        ws = _empty(need, torch.uint8, device)
-        args.workspace, args.workspace_bytes = ws.data_ptr(), need
-    ec._check(getattr(L, name)(ctypes.byref(args), ec._stream(None)), name)
-
-
 @_placed
 def gated_linear(x, w, bias=None, *, act="silu", x_scale=None, w_scale=None, out_scale=None, out_dtype=None,
                  save_preact=False, out=None, preact=None):
@@ -526,7 +520,8 @@ def gated_linear_backward(dy, x, w, preact, *, act="silu", need_dx=True, need_dw
     Returns (dx, dw, db), None where not needed: dx [m, k] bfloat16, dw
     [2n, k] in dw_dtype (bfloat16, or float32), db [2n] float32.  The gradient
     of preact is rounded to bfloat16 for the two products (not for db).  Sums
-    run in a fixed order: the same call gives the same bits."""
+    run in a fixed order: the same call gives the same bits.  Buffers given for
+    the results overlap nothing that is read."""
     return _gated_backward(dy, x, w, None, preact, act, need_dx, need_dw, need_db, dw_dtype, dx, dw, db, None)
 
 

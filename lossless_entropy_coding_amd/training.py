@@ -98,7 +98,8 @@ def linear_cross_entropy_backward(dloss, x, w, target, lse, *, ignore_index=-100
     and add nothing to dw, whatever x holds there.  The logits are computed
     again by pieces of the vocabulary, and their gradient is rounded to
     bfloat16 for the two products.  Sums run in a fixed order: the same call
-    gives the same bits."""
+    gives the same bits.  Buffers given for the results overlap nothing that is
+    read."""
     if not isinstance(dloss, torch.Tensor) or not dloss.is_cuda:
         _error("dloss must be a CUDA tensor")
     a, m, n, k, dev = _loss_args(x, w, target, ignore_index, status)
