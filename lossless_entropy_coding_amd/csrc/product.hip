@@ -187,7 +187,15 @@ Plan make_plan(const ProductArgs &a) {
     // The average decides, since the host does not know the offsets: 1024 rows
     // of which 962 are in one of 32 groups take 90 us so and 45 in tiles.
     const uint64_t rows = ragged ? ceil_div(a.I, groups) : a.I;
-    if (!outer_b && rows <= 32) {
+    // The loss reads its rows again for every 16 entries of the vocabulary, and
+    // with many of those, more than eight rows weigh more than the tiles' unused
+    // ones.  Maxima and sums so and in tiles (us): 8 rows by 32768 x 2048 40.3 and
+    // 42.2, 12 43.3 and 41.8, 16 47.0 and 42.4, 32 61.4 and 45.4; 32 by 131072 x 2048
+    // 217 and 140; 16 by 16384 x 4096 45.8 and 41.7, by 8192 x 4096 23.7 and 34.3.
+    // With gradients 32 by 32768 x 2048 184 and 152, by 8192 x 2048 64.7 and 72.9.
+    const bool logits = a.op == kOpRowStats || a.op == kOpLogitGrad;
+    const bool again = logits && rows > 8 && ceil_div(a.J, 16) >= 4 * kCUs;
+    if (!outer_b && rows <= 32 && !again) {
         const bool fill = ceil_div(a.J, 16) * groups >= (ragged ? 2 : 1) * kCUs;
         if (few(rows > 16 && fill ? 2 : 1)) return q;
     }

@@ -144,6 +144,7 @@ def _loss(m, n, k, seed, ignored):
     (3000, 50001, 130),         # dx: contraction n, split; dw: contraction m
     (8192, 2000, 1030),         # dx whole; logits of long rows; m the last that counts its rows by itself
     (8192, 2000, 2048), (9001, 1601, 2050),
+    (8, 16384, 136), (9, 16384, 136), (16, 16369, 40), (17, 20001, 2050), (32, 33000, 1000),    # few rows, and tiles
     (8192, 35001, 2048),        # two pieces, dx's sums carried from one to the other
 ], ids=str)
 @pytest.mark.parametrize("ignored", [0.1, 0.9])
