@@ -793,7 +793,7 @@ typedef struct ec_adamw_args {
 
 uint64_t adamw_state_blocks(uint64_t n);
 
-/* tensors: host memory, read before the call returns; 2^32 blocks together at most (EC_E_UNSUPPORTED beyond). */
+/* No two of the tensors and states overlap.  tensors: host memory, read before the call returns; 2^32 blocks together at most (EC_E_UNSUPPORTED beyond). */
 int adamw_step(const ec_adamw_tensor *tensors, uint32_t count, const ec_adamw_args *a, hipStream_t stream);
 
 /* Static text for an ec_error value or for a set of EC_S_* status bits. */
