@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 
 import _ffn  # noqa: E402
 import _training as tr  # noqa: E402
-from _ffn import F8, edges, near  # noqa: E402
+from _ffn import F8, edges, inside_nan, near  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -164,6 +164,26 @@ def test_loss(ec, m, n, k, ignored):
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
+@pytest.mark.parametrize("m,n,k", [(9, 16400, 65), (32, 17001, 71), (8, 16400, 65)], ids=str)
+def test_loss_of_few_strided_rows(ec, m, n, k):
+    """Rows at odd addresses in the middle of NaN: few rows read them in place, tiles from a copy."""
+    x, w, t, dl = _loss(m, n, k, 3, 0.2)
+    loss, lse = ec.linear_cross_entropy(inside_nan(x), inside_nan(w, left=1), t)
+    want, tol, want_lse, tol_lse, _, _ = tr.loss(x, w, t)
+    near(lse, want_lse, tol_lse, "lse")
+    near(loss, want, tol, "loss")
+    dx = inside_nan(torch.zeros(m, k, device="cuda").bfloat16())
+    dw = inside_nan(torch.zeros(n, k, device="cuda"), left=1)
+    ec.linear_cross_entropy_backward(dl, inside_nan(x), inside_nan(w, left=1), t, lse, dx=dx, dw=dw)
+    (wx, tx), (ww, tw) = tr.loss_backward(dl, x, w, t, dw_dtype=torch.float32)
+    near(dx, wx, tx, "dx")
+    near(dw, ww, tw, "dw")
+    for base, (rows, cols), left in ((dx._base, (m, k), 3), (dw._base, (n, k), 1)):
+        keep = torch.ones_like(base, dtype=torch.bool)
+        keep[2:2 + rows, left:left + cols] = False
+        assert bool(base[keep].isnan().all())
+
+
 @pytest.mark.parametrize("m", [8191, 8192, 8193, 20000])
 def test_rows_without_a_target(ec, m):
     """Up to 8192 rows and beyond, where another launch finds their places: targets outside the vocabulary are reported and
@@ -196,6 +216,33 @@ def test_rows_without_a_target(ec, m):
     t.fill_(-100)
     for a in ec.linear_cross_entropy_backward(dl, x, w, t, lse):
         assert bool((a == 0).all())
+
+
+def test_loss_of_few_rows_in_a_graph(ec):
+    """Captured where tiles are taken, with another number of rows that have a target in each replay."""
+    x, w, t, dl = _loss(24, 16500, 136, 5, 0.2)
+
+    def both():
+        loss, lse = ec.linear_cross_entropy(x, w, t)
+        return (loss, lse) + ec.linear_cross_entropy_backward(dl, x, w, t, lse)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = both()
+    for k, ignored in enumerate((0.0, 0.5, 1.0, 0.1)):
+        nx, _, nt, ndl = _loss(24, 16500, 136, 10 + k, ignored)
+        for to, new in ((x, nx), (t, nt), (dl, ndl)):
+            to.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager)), "replay %d" % k
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
